@@ -397,6 +397,128 @@ switch_status_t switch_ep_experts(const switch_config_t* cfg, const switch_ep_t*
                                   void* const* out_peers, void* ws, size_t ws_bytes,
                                   void* stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit block rows.  Some calls below hold rows in 8 bits: e4m3 values
+ * [rows, cols] (one byte each) and scales [rows, ceil(cols / 128)], one e8m0
+ * byte b (the power of two 2^(b - 127)) for each 128 consecutive columns of a
+ * row (the last block may be shorter); value = e4m3 * scale.  Weights have
+ * one scale for each block of 128 x 128: [N, ceil(rows / 128),
+ * ceil(cols / 128)].  The library makes a block's scale the smallest power of
+ * two s >= 2^-100 with max |v| <= 448 s and rounds v / s once, to nearest,
+ * ties to even; an all-zero block has s = 2^-100.  It reads any scale byte
+ * from 1 to 254 (products of scales beyond fp32's range overflow as fp32
+ * does); 255 (NaN) is unspecified. */
+
+/* Residual addition and root-mean-square norm, as used in front of the layer
+ * (fp32 arithmetic, rows of d_model; cfg->T, d_model and dtype apply, bf16 or
+ * fp32):
+ *   z = x + residual, rounded once to the dtype (residual NULL: z = x),
+ *   rstd = 1 / sqrt(mean(z^2) + eps),   y = z * rstd * gain.
+ *   x [T, d_model]; residual [T, d_model] or NULL; gain [d_model] fp32 or NULL
+ *   (ones); eps >= 0;
+ *   z [T, d_model] out or NULL; y [T, d_model] out or NULL; yq [T, d_model] and
+ *   y_scale [T, ceil(d_model / 128)]: y as 8-bit block rows (from the fp32
+ *   value, rounded once), or both NULL; y or yq must be given; rstd [T] fp32
+ *   out or NULL (the backward needs it).
+ * z may be the buffer of x or of residual. */
+switch_status_t switch_residual_norm(const switch_config_t* cfg, const void* x,
+                                     const void* residual, const float* gain, float eps, void* z,
+                                     void* y, void* yq, void* y_scale, float* rstd, void* stream);
+
+/* Backward of switch_residual_norm.  z and rstd as the forward left them (z is
+ * x where there was no residual), dy [T, d_model] the gradient of y, dsum
+ * [T, d_model] or NULL the gradient that reaches z by other ways (the residual
+ * stream), both in the dtype:
+ *   t = dy * gain,   dx = rstd t - z rstd^3 mean(t z) (+ dsum),
+ *   dgain = sum over rows of dy z rstd.
+ *   dx [T, d_model] out (the gradient of x and of residual alike) or NULL;
+ *   dgain [d_model] fp32 out or NULL; one of them must be given.
+ * dx may be the buffer of dy or of dsum.  dgain needs a workspace of
+ * switch_norm_workspace_size() bytes (256-byte aligned; nothing in it has to
+ * be zero or is kept; else ws may be NULL); its sums have a fixed order (bit-
+ * reproducible on one kind of GPU).  T = 0 writes nothing, dgain neither. */
+switch_status_t switch_residual_norm_backward(const switch_config_t* cfg, const void* z,
+                                              const float* gain, const float* rstd, const void* dy,
+                                              const void* dsum, void* dx, float* dgain, void* ws,
+                                              size_t ws_bytes, void* stream);
+switch_status_t switch_norm_workspace_size(const switch_config_t* cfg, size_t* bytes);
+
+/* Expert weights (bf16) as 8-bit blocks: w1 [N, d_ff, d_model] into w1q (same
+ * shape, one byte each) and w1_scale [N, ceil(d_ff / 128),
+ * ceil(d_model / 128)], w2 likewise.  w1 or w2 may be NULL (then its outputs
+ * are not used).  cfg->T has no effect. */
+switch_status_t switch_quantize_weights(const switch_config_t* cfg, const void* w1, const void* w2,
+                                        void* w1q, void* w1_scale, void* w2q, void* w2_scale,
+                                        void* stream);
+
+/* switch_expert_ffn on 8-bit rows and weights:
+ *   h[e, r, :] = relu(x[slot_token[e*C + r]] . w1[e]^T), as 8-bit block rows,
+ *   y[e, r, :] = h[e, r, :] . w2[e]^T   for r < n_e = min(counts[e], C);
+ * rows r >= n_e of y are left untouched.  xq [T, d_model] and x_scale
+ * [T, ceil(d_model / 128)] (from switch_residual_norm), weights from
+ * switch_quantize_weights, y [N, C, d_model] bf16.  Products on the tensor
+ * cores with fp32 sums; h is rounded once, to 8 bits, y once, to bf16.  With
+ * SWITCH_FLAG_ROWS_DISPATCHED xq and x_scale are the slots' rows [N*C, ...]
+ * and slot_token is not read.  A token of a kept slot outside [0, T) sets
+ * SWITCH_ERR_DEVICE_BOUNDS in the error word (its row counts as zeros).
+ * cfg->dtype SWITCH_BF16 only; workspace switch_workspace_size(). */
+switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
+                                     const void* x_scale, const int32_t* slot_token,
+                                     const int32_t* counts, const void* w1q, const void* w1_scale,
+                                     const void* w2q, const void* w2_scale, void* y, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/* switch_expert_ffn (bf16) that keeps what its backward needs in 8 bits:
+ *   xq [N*C, d_model], x_scale: the slots' rows of x as 8-bit block rows;
+ *   hq [N*C, d_ff], h_scale: the hidden rows (after ReLU, rounded to bf16) as
+ *   8-bit block rows in which a value above zero never becomes zero (it takes
+ *   the smallest e4m3 value, 2^-9 times its scale), so hq > 0 is the ReLU's
+ *   mask.
+ * y is switch_expert_ffn's.  Rows r >= n_e of all outputs are left untouched.
+ * x, slot_token and SWITCH_FLAG_ROWS_DISPATCHED as for switch_expert_ffn (the
+ * rows are always copied: SWITCH_FLAG_GATHER_IN_GEMM has no effect).
+ * cfg->dtype SWITCH_BF16 only; workspace switch_workspace_size(). */
+switch_status_t switch_expert_ffn_checkpoint(const switch_config_t* cfg, const void* x,
+                                             const int32_t* slot_token, const int32_t* counts,
+                                             const void* w1, const void* w2, void* y, void* xq,
+                                             void* x_scale, void* hq, void* h_scale, void* ws,
+                                             size_t ws_bytes, void* stream);
+
+/* Backward of the expert FFNs from those rows: with x and h the values of the
+ * 8-bit rows and dy [N, C, d_model] bf16 the gradient of y, per expert over its
+ * n_e rows,
+ *   da = (dy w2[e]) where h > 0,   dx = da w1[e],
+ *   dw1[e] = da^T x,   dw2[e] = dy^T h.
+ *   dx [N, C, d_model], dw1 [N, d_ff, d_model], dw2 [N, d_model, d_ff] bf16.
+ * Rows r >= n_e of the inputs may hold anything, those of dx are left
+ * untouched; an expert without tokens has zero weight gradients.  fp32 sums, da
+ * rounded once to bf16.  cfg->dtype SWITCH_BF16 only; workspace
+ * switch_backward_workspace_size(). */
+switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const void* xq,
+                                              const void* x_scale, const void* hq,
+                                              const void* h_scale, const int32_t* counts,
+                                              const void* w1, const void* w2, const void* dy,
+                                              void* dx, void* dw1, void* dw2, void* ws,
+                                              size_t ws_bytes, void* stream);
+
+/* The layer's kept state in 8 bits.  switch_layer_forward with
+ * SWITCH_FLAG_TRAINING keeps its routing, probabilities and hidden rows in the
+ * workspace until the backward; between the two, switch_checkpoint_save copies
+ * them into `ckpt` (switch_checkpoint_size() bytes, 256-byte aligned; the hidden
+ * rows as 8-bit block rows as above), after which the workspace may serve
+ * other layers and calls, and switch_checkpoint_load puts them back into a
+ * workspace, followed by switch_layer_backward with SWITCH_FLAG_TRAINING.  Both
+ * take the forward's config; load also its x (the dispatched rows are copied
+ * from it again, exactly).  The gradients are then those of the rounded hidden
+ * rows; the ReLU's mask, the routing and the probabilities are exact.
+ * Workspaces of switch_backward_workspace_size() bytes; SWITCH_FLAG_TRAINING
+ * must be set; cfg->dtype SWITCH_BF16 only. */
+switch_status_t switch_checkpoint_size(const switch_config_t* cfg, size_t* bytes);
+switch_status_t switch_checkpoint_save(const switch_config_t* cfg, const void* ws, size_t ws_bytes,
+                                       void* ckpt, size_t ckpt_bytes, void* stream);
+switch_status_t switch_checkpoint_load(const switch_config_t* cfg, const void* x, const void* ckpt,
+                                       size_t ckpt_bytes, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, reads the workspace's device error word, clears
  * it, and returns the recorded status (SWITCH_OK if none).  *where_out and
  * *info_out (either may be NULL) receive the reporting kernel role and a

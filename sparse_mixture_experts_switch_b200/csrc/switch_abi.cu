@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "backward.cuh"
+#include "q8.cuh"
 
 using namespace smoe;
 
@@ -958,6 +959,350 @@ switch_status_t switch_ep_experts(const switch_config_t* cfg, const switch_ep_t*
   a.spin = c.spin;
   a.num_sms = c.num_sms;
   return cuda_status(launch_expert_ffn_bf16(a, c.st));
+}
+
+// ------------------------------------------------- norm and 8-bit rows
+
+switch_status_t switch_norm_workspace_size(const switch_config_t* cfg, size_t* bytes) {
+  switch_status_t s = validate(cfg, nullptr);
+  if (s != SWITCH_OK) return s;
+  if (bytes == nullptr) return SWITCH_ERR_INVALID_ARG;
+  *bytes = 256 + sizeof(float) * kNormParts * static_cast<size_t>(cfg->d_model);
+  return SWITCH_OK;
+}
+
+switch_status_t switch_residual_norm(const switch_config_t* cfg, const void* x,
+                                     const void* residual, const float* gain, float eps, void* z,
+                                     void* y, void* yq, void* y_scale, float* rstd, void* stream) {
+  switch_status_t s = validate(cfg, nullptr);
+  if (s != SWITCH_OK) return s;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return SWITCH_ERR_INVALID_ARG;
+  if (cfg->T == 0) return SWITCH_OK;
+  if (!x || (!y && !yq) || (yq == nullptr) != (y_scale == nullptr) || !aligned16(x) ||
+      !aligned16(residual) || !aligned16(gain) || !aligned16(z) || !aligned16(y) || !aligned16(yq))
+    return SWITCH_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  if (sms <= 0) return sms == 0 ? SWITCH_ERR_CUDA : SWITCH_ERR_UNSUPPORTED;
+  NormArgs a{};
+  a.T = cfg->T;
+  a.d = cfg->d_model;
+  a.bf16 = cfg->dtype == SWITCH_BF16;
+  a.x = x;
+  a.residual = residual;
+  a.gain = gain;
+  a.eps = eps;
+  a.z = z;
+  a.y = y;
+  a.yq = static_cast<uint8_t*>(yq);
+  a.ys = static_cast<uint8_t*>(y_scale);
+  a.rstd = rstd;
+  a.num_sms = sms;
+  return cuda_status(launch_residual_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+switch_status_t switch_residual_norm_backward(const switch_config_t* cfg, const void* z,
+                                              const float* gain, const float* rstd, const void* dy,
+                                              const void* dsum, void* dx, float* dgain, void* ws,
+                                              size_t ws_bytes, void* stream) {
+  switch_status_t s = validate(cfg, nullptr);
+  if (s != SWITCH_OK || cfg->T == 0) return s;
+  if (!z || !rstd || !dy || (!dx && !dgain) || !aligned16(z) || !aligned16(gain) ||
+      !aligned16(dy) || !aligned16(dsum) || !aligned16(dx))
+    return SWITCH_ERR_INVALID_ARG;
+  size_t need = 0;
+  switch_norm_workspace_size(cfg, &need);
+  if (dgain) {
+    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+      return SWITCH_ERR_INVALID_ARG;
+    if (ws_bytes < need) return SWITCH_ERR_WORKSPACE_TOO_SMALL;
+  }
+  const int sms = device_sms();
+  if (sms <= 0) return sms == 0 ? SWITCH_ERR_CUDA : SWITCH_ERR_UNSUPPORTED;
+  NormBwdArgs a{};
+  a.T = cfg->T;
+  a.d = cfg->d_model;
+  a.bf16 = cfg->dtype == SWITCH_BF16;
+  a.z = z;
+  a.gain = gain;
+  a.rstd = rstd;
+  a.dy = dy;
+  a.dsum = dsum;
+  a.dx = dx;
+  a.dgain = dgain;
+  if (dgain) a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
+  a.num_sms = sms;
+  return cuda_status(launch_residual_norm_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+// Config of the calls on 8-bit rows: bf16 layers only.
+static switch_status_t validate_q8(const switch_config_t* cfg, int64_t* C = nullptr) {
+  const switch_status_t s = validate(cfg, C);
+  if (s != SWITCH_OK) return s;
+  return cfg->dtype == SWITCH_BF16 ? SWITCH_OK : SWITCH_ERR_UNSUPPORTED;
+}
+// The workspace of the calls that need switch_backward_workspace_size bytes.
+static switch_status_t check_bwd_workspace(const switch_config_t* cfg, int64_t C, const void* ws,
+                                           size_t ws_bytes) {
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return SWITCH_ERR_INVALID_ARG;
+  return ws_bytes < layout_for(*cfg, C).bwd_total ? SWITCH_ERR_WORKSPACE_TOO_SMALL : SWITCH_OK;
+}
+
+switch_status_t switch_quantize_weights(const switch_config_t* cfg, const void* w1, const void* w2,
+                                        void* w1q, void* w1_scale, void* w2q, void* w2_scale,
+                                        void* stream) {
+  const switch_status_t s = validate_q8(cfg);
+  if (s != SWITCH_OK) return s;
+  if (!w1 && !w2) return SWITCH_ERR_INVALID_ARG;
+  if ((w1 && (!w1q || !w1_scale)) || (w2 && (!w2q || !w2_scale)) || !aligned16(w1) ||
+      !aligned16(w2) || !aligned16(w1q) || !aligned16(w2q))
+    return SWITCH_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  if (sms <= 0) return sms == 0 ? SWITCH_ERR_CUDA : SWITCH_ERR_UNSUPPORTED;
+  auto st = static_cast<cudaStream_t>(stream);
+  if (w1)
+    SMOE_TRY(launch_quantize_weights(cfg->n_experts, cfg->d_ff, cfg->d_model, w1,
+                                     static_cast<uint8_t*>(w1q), static_cast<uint8_t*>(w1_scale),
+                                     st));
+  if (w2)
+    SMOE_TRY(launch_quantize_weights(cfg->n_experts, cfg->d_model, cfg->d_ff, w2,
+                                     static_cast<uint8_t*>(w2q), static_cast<uint8_t*>(w2_scale),
+                                     st));
+  return SWITCH_OK;
+}
+
+switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
+                                     const void* x_scale, const int32_t* slot_token,
+                                     const int32_t* counts, const void* w1q, const void* w1_scale,
+                                     const void* w2q, const void* w2_scale, void* y, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  Ctx c{};
+  switch_status_t s = validate_q8(cfg);
+  if (s != SWITCH_OK || cfg->T == 0) return s;
+  const bool dispatched = (cfg->flags & SWITCH_FLAG_ROWS_DISPATCHED) != 0;
+  if (!xq || !x_scale || (!slot_token && !dispatched) || !counts || !w1q || !w1_scale || !w2q ||
+      !w2_scale || !y || !aligned16(xq) || !aligned16(x_scale) || !aligned16(w1q) ||
+      !aligned16(w1_scale) || !aligned16(w2q) || !aligned16(w2_scale) || !aligned16(y))
+    return SWITCH_ERR_INVALID_ARG;
+  s = prepare(cfg, ws, ws_bytes, stream, &c);
+  if (s != SWITCH_OK) return s;
+  const int64_t S = static_cast<int64_t>(cfg->n_experts) * c.C;
+  FfnQ8Args a{};
+  a.A = routes_of(*cfg) * cfg->T;
+  a.d = cfg->d_model;
+  a.F = cfg->d_ff;
+  a.N = cfg->n_experts;
+  a.C = c.C;
+  a.counts = counts;
+  a.xq = static_cast<const uint8_t*>(xq);
+  a.xs = static_cast<const uint8_t*>(x_scale);
+  if (!dispatched) {
+    // the slots' rows and, behind them, their scales (d_model / 128 bytes of
+    // a row's d_model that the 16-bit region has left)
+    uint8_t* q = c.at<uint8_t>(c.L.xdisp);
+    uint8_t* sc = q + S * cfg->d_model;
+    SMOE_TRY(launch_gather_rows_q8(S, cfg->d_model, slot_token, a.xq, a.xs, counts, c.C, cfg->T, q,
+                                   sc, c.err, c.st));
+    a.xq = q;
+    a.xs = sc;
+  }
+  a.w1q = static_cast<const uint8_t*>(w1q);
+  a.w1s = static_cast<const uint8_t*>(w1_scale);
+  a.w2q = static_cast<const uint8_t*>(w2q);
+  a.w2s = static_cast<const uint8_t*>(w2_scale);
+  a.hq = c.at<uint8_t>(c.L.hbuf);
+  a.hs = a.hq + S * cfg->d_ff;
+  a.y = y;
+  a.err = c.err;
+  a.spin = c.spin;
+  a.num_sms = c.num_sms;
+  return cuda_status(launch_expert_ffn_q8(a, c.st));
+}
+
+switch_status_t switch_expert_ffn_checkpoint(const switch_config_t* cfg, const void* x,
+                                             const int32_t* slot_token, const int32_t* counts,
+                                             const void* w1, const void* w2, void* y, void* xq,
+                                             void* x_scale, void* hq, void* h_scale, void* ws,
+                                             size_t ws_bytes, void* stream) {
+  Ctx c{};
+  switch_status_t s = validate_q8(cfg);
+  if (s != SWITCH_OK || cfg->T == 0) return s;
+  const bool dispatched = (cfg->flags & SWITCH_FLAG_ROWS_DISPATCHED) != 0;
+  if (!x || (!slot_token && !dispatched) || !counts || !w1 || !w2 || !y || !xq || !x_scale ||
+      !hq || !h_scale || !aligned16(x) || !aligned16(w1) || !aligned16(w2) || !aligned16(y) ||
+      !aligned16(xq) || !aligned16(x_scale) || !aligned16(hq) || !aligned16(h_scale))
+    return SWITCH_ERR_INVALID_ARG;
+  s = prepare(cfg, ws, ws_bytes, stream, &c);
+  if (s != SWITCH_OK) return s;
+  const int64_t S = static_cast<int64_t>(cfg->n_experts) * c.C;
+  FfnArgs a{};
+  a.T = cfg->T;
+  a.d = cfg->d_model;
+  a.F = cfg->d_ff;
+  a.N = cfg->n_experts;
+  a.C = c.C;
+  a.slot_token = slot_token;
+  a.counts = counts;
+  a.mtile_start = c.at<int>(c.L.mtile_start);
+  a.w1 = w1;
+  a.w2 = w2;
+  a.hbuf = c.ws + c.L.hbuf;
+  a.y = y;
+  a.mode2 = kModeY;
+  a.err = c.err;
+  a.spin = c.spin;
+  a.num_sms = c.num_sms;
+  a.pair1 = (cfg->flags & SWITCH_FLAG_GEMM_PAIRS) != 0;
+  a.pair2 = !(cfg->flags & SWITCH_FLAG_GEMM_1SM);
+  switch_config_t by_copy = *cfg;            // the rows are always copied here
+  by_copy.flags &= ~SWITCH_FLAG_GATHER_IN_GEMM;
+  a.pair1_rows = gemm1_rows_pairs(&by_copy, c.C);
+  a.x_disp = dispatched ? x : c.ws + c.L.xdisp;
+  SMOE_TRY(launch_mtile_table(a.N, a.C, counts, c.at<int>(c.L.mtile_start), c.st));
+  SMOE_TRY(launch_quantize_rows(S, a.d, x, counts, c.C, dispatched ? nullptr : slot_token, cfg->T,
+                                dispatched ? nullptr : c.ws + c.L.xdisp, false,
+                                static_cast<uint8_t*>(xq), static_cast<uint8_t*>(x_scale), c.err,
+                                c.st));
+  SMOE_TRY(launch_expert_ffn_bf16(a, c.st));
+  return cuda_status(launch_quantize_rows(S, a.F, a.hbuf, counts, c.C, nullptr, 0, nullptr, true,
+                                          static_cast<uint8_t*>(hq),
+                                          static_cast<uint8_t*>(h_scale), c.err, c.st));
+}
+
+switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const void* xq,
+                                              const void* x_scale, const void* hq,
+                                              const void* h_scale, const int32_t* counts,
+                                              const void* w1, const void* w2, const void* dy,
+                                              void* dx, void* dw1, void* dw2, void* ws,
+                                              size_t ws_bytes, void* stream) {
+  Ctx c{};
+  int64_t C = 0;
+  switch_status_t s = validate_q8(cfg, &C);
+  if (s != SWITCH_OK || cfg->T == 0) return s;
+  if (!xq || !x_scale || !hq || !h_scale || !counts || !w1 || !w2 || !dy || !dx || !dw1 || !dw2 ||
+      !aligned16(xq) || !aligned16(x_scale) || !aligned16(hq) || !aligned16(h_scale) ||
+      !aligned16(w1) || !aligned16(w2) || !aligned16(dy) || !aligned16(dx) || !aligned16(dw1) ||
+      !aligned16(dw2))
+    return SWITCH_ERR_INVALID_ARG;
+  s = check_bwd_workspace(cfg, C, ws, ws_bytes);
+  if (s != SWITCH_OK) return s;
+  s = prepare(cfg, ws, ws_bytes, stream, &c);
+  if (s != SWITCH_OK) return s;
+  const int64_t S = static_cast<int64_t>(cfg->n_experts) * c.C;
+  BwdFfnArgs b{};
+  b.T = cfg->T;
+  b.d = cfg->d_model;
+  b.F = cfg->d_ff;
+  b.N = cfg->n_experts;
+  b.C = c.C;
+  b.counts = counts;
+  b.mtile_start = c.at<int>(c.L.mtile_start);
+  b.w1 = w1;
+  b.w2 = w2;
+  b.x_disp = c.ws + c.L.xdisp;
+  b.hbuf = c.ws + c.L.hbuf;
+  b.dys = c.ws + c.L.ybuf;
+  b.da = c.ws + c.L.da;
+  b.dgp = c.at<float>(c.L.dgp);
+  b.dw1 = dw1;
+  b.dw2 = dw2;
+  b.dx = dx;
+  b.pair_dw = !(cfg->flags & SWITCH_FLAG_GEMM_1SM);
+  b.err = c.err;
+  b.spin = c.spin;
+  b.num_sms = c.num_sms;
+  SMOE_TRY(launch_mtile_table(b.N, b.C, counts, c.at<int>(c.L.mtile_start), c.st));
+  SMOE_TRY(launch_unpack_rows(S, b.d, static_cast<const uint8_t*>(xq),
+                              static_cast<const uint8_t*>(x_scale), counts, c.C,
+                              c.ws + c.L.xdisp, c.st));
+  SMOE_TRY(launch_unpack_rows(S, b.F, static_cast<const uint8_t*>(hq),
+                              static_cast<const uint8_t*>(h_scale), counts, c.C,
+                              c.ws + c.L.hbuf, c.st));
+  SMOE_TRY(launch_copy_kept_rows(S, b.d, dy, counts, c.C, c.ws + c.L.ybuf, c.st));
+  SMOE_TRY(launch_bwd_dh(b, c.st));
+  SMOE_TRY(launch_bwd_dw(b, c.st));
+  return cuda_status(launch_bwd_dx_rows(b, c.st));
+}
+
+// What switch_layer_forward (SWITCH_FLAG_TRAINING) keeps, outside the
+// workspace: the routing arrays (one range of the workspace, from idx to the
+// tile table), the router probabilities, and H as 8-bit rows.
+struct CkptLayout {
+  size_t routing, routing_bytes, probs, probs_bytes, hq, hs, total;
+};
+static CkptLayout ckpt_layout(const switch_config_t& c, int64_t C, const Layout& L) {
+  const size_t S = static_cast<size_t>(c.n_experts) * static_cast<size_t>(C);
+  CkptLayout k{};
+  k.routing = 0;
+  k.routing_bytes = L.wsplit - L.idx;
+  k.probs = align_up(k.routing_bytes, 256);
+  k.probs_bytes = sizeof(float) * c.n_experts * static_cast<size_t>(c.T);
+  k.hq = align_up(k.probs + k.probs_bytes, 256);
+  k.hs = align_up(k.hq + S * c.d_ff, 256);
+  k.total = align_up(k.hs + S * q8_blocks(c.d_ff), 256);
+  return k;
+}
+
+switch_status_t switch_checkpoint_size(const switch_config_t* cfg, size_t* bytes) {
+  int64_t C = 0;
+  const switch_status_t s = validate_q8(cfg, &C);
+  if (s != SWITCH_OK) return s;
+  if (bytes == nullptr) return SWITCH_ERR_INVALID_ARG;
+  *bytes = ckpt_layout(*cfg, C, layout_for(*cfg, C)).total;
+  return SWITCH_OK;
+}
+
+switch_status_t switch_checkpoint_save(const switch_config_t* cfg, const void* ws, size_t ws_bytes,
+                                       void* ckpt, size_t ckpt_bytes, void* stream) {
+  Ctx c{};
+  int64_t C = 0;
+  switch_status_t s = validate_q8(cfg, &C);
+  if (s != SWITCH_OK || cfg->T == 0) return s;
+  if (!(cfg->flags & SWITCH_FLAG_TRAINING) || !ckpt ||
+      (reinterpret_cast<uintptr_t>(ckpt) & 255u) != 0)
+    return SWITCH_ERR_INVALID_ARG;
+  const CkptLayout k = ckpt_layout(*cfg, C, layout_for(*cfg, C));
+  s = check_bwd_workspace(cfg, C, ws, ws_bytes);
+  if (s != SWITCH_OK) return s;
+  if (ckpt_bytes < k.total) return SWITCH_ERR_WORKSPACE_TOO_SMALL;
+  s = prepare(cfg, const_cast<void*>(ws), ws_bytes, stream, &c);
+  if (s != SWITCH_OK) return s;
+  auto* out = static_cast<uint8_t*>(ckpt);
+  SMOE_TRY(cudaMemcpyAsync(out + k.routing, c.ws + c.L.idx, k.routing_bytes,
+                           cudaMemcpyDeviceToDevice, c.st));
+  SMOE_TRY(cudaMemcpyAsync(out + k.probs, c.ws + c.L.probs_s, k.probs_bytes,
+                           cudaMemcpyDeviceToDevice, c.st));
+  return cuda_status(launch_quantize_rows(static_cast<int64_t>(cfg->n_experts) * c.C, cfg->d_ff,
+                                          c.ws + c.L.hbuf, c.at<int>(c.L.counts), c.C, nullptr, 0,
+                                          nullptr, true, out + k.hq, out + k.hs, c.err, c.st));
+}
+
+switch_status_t switch_checkpoint_load(const switch_config_t* cfg, const void* x, const void* ckpt,
+                                       size_t ckpt_bytes, void* ws, size_t ws_bytes,
+                                       void* stream) {
+  Ctx c{};
+  int64_t C = 0;
+  switch_status_t s = validate_q8(cfg, &C);
+  if (s != SWITCH_OK || cfg->T == 0) return s;
+  if (!(cfg->flags & SWITCH_FLAG_TRAINING) || !x || !aligned16(x) || !ckpt ||
+      (reinterpret_cast<uintptr_t>(ckpt) & 255u) != 0)
+    return SWITCH_ERR_INVALID_ARG;
+  const CkptLayout k = ckpt_layout(*cfg, C, layout_for(*cfg, C));
+  s = check_bwd_workspace(cfg, C, ws, ws_bytes);
+  if (s != SWITCH_OK) return s;
+  if (ckpt_bytes < k.total) return SWITCH_ERR_WORKSPACE_TOO_SMALL;
+  s = prepare(cfg, ws, ws_bytes, stream, &c);
+  if (s != SWITCH_OK) return s;
+  const int64_t S = static_cast<int64_t>(cfg->n_experts) * c.C;
+  const auto* in = static_cast<const uint8_t*>(ckpt);
+  SMOE_TRY(cudaMemcpyAsync(c.ws + c.L.idx, in + k.routing, k.routing_bytes,
+                           cudaMemcpyDeviceToDevice, c.st));
+  SMOE_TRY(cudaMemcpyAsync(c.ws + c.L.probs_s, in + k.probs, k.probs_bytes,
+                           cudaMemcpyDeviceToDevice, c.st));
+  SMOE_TRY(launch_gather_rows(S, static_cast<int64_t>(cfg->d_model) * 2,
+                              c.at<int>(c.L.slot_token), x, c.ws + c.L.xdisp, c.st));
+  return cuda_status(launch_unpack_rows(S, cfg->d_ff, in + k.hq, in + k.hs,
+                                        c.at<int>(c.L.counts), c.C, c.ws + c.L.hbuf, c.st));
 }
 
 switch_status_t switch_get_device_error(void* ws, void* stream, int32_t* where_out,

@@ -96,6 +96,21 @@ def _load():
                                          c_void_p, c_size_t, c_void_p]),
         "switch_ep_experts": (c_int32, [cfgp, POINTER(SwitchEp), c_void_p, c_void_p, c_void_p,
                                         POINTER(c_void_p), c_void_p, c_size_t, c_void_p]),
+        "switch_norm_workspace_size": (c_int32, [cfgp, POINTER(c_size_t)]),
+        "switch_residual_norm": (c_int32, [cfgp, c_void_p, c_void_p, c_void_p, c_float, c_void_p,
+                                           c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+        "switch_residual_norm_backward": (c_int32, [cfgp, c_void_p, c_void_p, c_void_p, c_void_p,
+                                                    c_void_p, c_void_p, c_void_p, c_void_p,
+                                                    c_size_t, c_void_p]),
+        "switch_quantize_weights": (c_int32, [cfgp] + [c_void_p] * 7),
+        "switch_expert_ffn_q8": (c_int32, [cfgp] + [c_void_p] * 10 + [c_size_t, c_void_p]),
+        "switch_expert_ffn_checkpoint": (c_int32, [cfgp] + [c_void_p] * 11 + [c_size_t, c_void_p]),
+        "switch_expert_ffn_backward_q8": (c_int32, [cfgp] + [c_void_p] * 12 + [c_size_t, c_void_p]),
+        "switch_checkpoint_size": (c_int32, [cfgp, POINTER(c_size_t)]),
+        "switch_checkpoint_save": (c_int32, [cfgp, c_void_p, c_size_t, c_void_p, c_size_t,
+                                             c_void_p]),
+        "switch_checkpoint_load": (c_int32, [cfgp, c_void_p, c_void_p, c_size_t, c_void_p, c_size_t,
+                                             c_void_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -261,6 +276,109 @@ def switch_ep_experts(cfg, ep_, w1_local, w2_local, recv, out_peers, ws, stream=
     _check(_lib.switch_ep_experts(ctypes.byref(cfg), ctypes.byref(ep_), _p(w1_local),
                                   _p(w2_local), _p(recv), _ptr_array(out_peers), _p(ws),
                                   ws.numel(), _stream(stream)), "switch_ep_experts")
+
+
+# ------------------------------------------------- norm and 8-bit rows
+# 8-bit rows are float8_e4m3fn values [rows, cols] with float8_e8m0fnu scales
+# [rows, ceil(cols / 128)] (tensors of any one-byte type are taken).
+
+def switch_norm_workspace_size(cfg):
+    n = c_size_t(0)
+    _check(_lib.switch_norm_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "switch_norm_workspace_size")
+    return n.value
+
+
+def norm_workspace(cfg, device="cuda"):
+    """A device workspace of switch_norm_workspace_size(cfg) bytes."""
+    return torch.zeros(switch_norm_workspace_size(cfg), dtype=torch.uint8, device=device)
+
+
+def scale_blocks(cols):
+    """Scales of a row of `cols` columns: ceil(cols / 128)."""
+    return (cols + 127) // 128
+
+
+def q8_rows(rows, cols, device="cuda"):
+    """Buffers for 8-bit rows: e4m3 [rows, cols] (zeros) and e8m0 scales
+    [rows, ceil(cols / 128)] (ones)."""
+    q = torch.zeros(rows, cols, dtype=torch.uint8, device=device)
+    s = torch.full((rows, scale_blocks(cols)), 127, dtype=torch.uint8, device=device)
+    return q.view(torch.float8_e4m3fn), s.view(torch.float8_e8m0fnu)
+
+
+def q8_weights(n, rows, cols, device="cuda"):
+    """Buffers for 8-bit weights: e4m3 [n, rows, cols] and e8m0 scales
+    [n, ceil(rows / 128), ceil(cols / 128)]."""
+    q = torch.zeros(n, rows, cols, dtype=torch.uint8, device=device)
+    s = torch.full((n, scale_blocks(rows), scale_blocks(cols)), 127, dtype=torch.uint8,
+                   device=device)
+    return q.view(torch.float8_e4m3fn), s.view(torch.float8_e8m0fnu)
+
+
+def switch_residual_norm(cfg, x, residual, gain, eps, z, y, yq, y_scale, rstd, stream=None):
+    _check(_lib.switch_residual_norm(ctypes.byref(cfg), _p(x), _p(residual), _p(gain), float(eps),
+                                     _p(z), _p(y), _p(yq), _p(y_scale), _p(rstd),
+                                     _stream(stream)), "switch_residual_norm")
+
+
+def switch_residual_norm_backward(cfg, z, gain, rstd, dy, dsum, dx, dgain, ws, stream=None):
+    _check(_lib.switch_residual_norm_backward(ctypes.byref(cfg), _p(z), _p(gain), _p(rstd), _p(dy),
+                                              _p(dsum), _p(dx), _p(dgain), _p(ws),
+                                              0 if ws is None else ws.numel(), _stream(stream)),
+           "switch_residual_norm_backward")
+
+
+def switch_quantize_weights(cfg, w1, w2, w1q, w1_scale, w2q, w2_scale, stream=None):
+    _check(_lib.switch_quantize_weights(ctypes.byref(cfg), _p(w1), _p(w2), _p(w1q), _p(w1_scale),
+                                        _p(w2q), _p(w2_scale), _stream(stream)),
+           "switch_quantize_weights")
+
+
+def switch_expert_ffn_q8(cfg, xq, x_scale, slot_token, counts, w1q, w1_scale, w2q, w2_scale, y, ws,
+                         stream=None):
+    _check(_lib.switch_expert_ffn_q8(ctypes.byref(cfg), _p(xq), _p(x_scale), _p(slot_token),
+                                     _p(counts), _p(w1q), _p(w1_scale), _p(w2q), _p(w2_scale),
+                                     _p(y), _p(ws), ws.numel(), _stream(stream)),
+           "switch_expert_ffn_q8")
+
+
+def switch_expert_ffn_checkpoint(cfg, x, slot_token, counts, w1, w2, y, xq, x_scale, hq, h_scale, ws,
+                                 stream=None):
+    _check(_lib.switch_expert_ffn_checkpoint(ctypes.byref(cfg), _p(x), _p(slot_token), _p(counts),
+                                             _p(w1), _p(w2), _p(y), _p(xq), _p(x_scale), _p(hq),
+                                             _p(h_scale), _p(ws), ws.numel(), _stream(stream)),
+           "switch_expert_ffn_checkpoint")
+
+
+def switch_expert_ffn_backward_q8(cfg, xq, x_scale, hq, h_scale, counts, w1, w2, dy, dx, dw1, dw2,
+                                  ws, stream=None):
+    _check(_lib.switch_expert_ffn_backward_q8(ctypes.byref(cfg), _p(xq), _p(x_scale), _p(hq),
+                                              _p(h_scale), _p(counts), _p(w1), _p(w2), _p(dy),
+                                              _p(dx), _p(dw1), _p(dw2), _p(ws), ws.numel(),
+                                              _stream(stream)), "switch_expert_ffn_backward_q8")
+
+
+def switch_checkpoint_size(cfg):
+    n = c_size_t(0)
+    _check(_lib.switch_checkpoint_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "switch_checkpoint_size")
+    return n.value
+
+
+def checkpoint(cfg, device="cuda"):
+    """A device buffer of switch_checkpoint_size(cfg) bytes."""
+    return torch.empty(max(switch_checkpoint_size(cfg), 1), dtype=torch.uint8, device=device)
+
+
+def switch_checkpoint_save(cfg, ws, ckpt, stream=None):
+    _check(_lib.switch_checkpoint_save(ctypes.byref(cfg), _p(ws), ws.numel(), _p(ckpt),
+                                       ckpt.numel(), _stream(stream)), "switch_checkpoint_save")
+
+
+def switch_checkpoint_load(cfg, x, ckpt, ws, stream=None):
+    _check(_lib.switch_checkpoint_load(ctypes.byref(cfg), _p(x), _p(ckpt), ckpt.numel(), _p(ws),
+                                       ws.numel(), _stream(stream)), "switch_checkpoint_load")
 
 
 def switch_get_device_error(ws, stream=None):
