@@ -2,7 +2,7 @@
 //
 //   h = relu(x W1_e^T),  (hq, hs) = 8-bit rows of h,  y = h W2_e^T (bf16)
 //
-//   D[r, f] = sum over blocks k of 2^(sa[r, k] + sw[f / 128, k]) sum_j a[r, k, j] w[f, k, j]
+//   D[f, t] = sum over blocks k of 2^(sw[f / 128, k] + sa[t, k]) sum_j w[f, k, j] a[t, k, j]
 //
 // The tensor core applies the scales itself: tcgen05.mma.kind::mxf8f6f4 with
 // block_scale multiplies each 32-deep step by one e8m0 scale of each operand
@@ -12,20 +12,31 @@
 // 512 columns, exactly four consecutive bytes of the row-major scale array.
 // Products and sums are fp32 in TMEM.
 //
-// One persistent kernel for both products: tile = 128 slots x BN columns, K in
-// blocks of 128 bytes through a ring of TMA stages.
-//   * warp 0 loads the row and weight tiles by TMA (128-byte swizzle);
-//   * warp 2 brings the scales: for each 512 columns the 128 rows' words, laid
-//     out as tcgen05.cp wants them (row r at lane r % 32, word r / 32), and one
-//     word for each 128 weight rows, repeated;
-//   * warp 1 copies the scales to TMEM (tcgen05.cp) and issues the MMAs;
-//   * warps 4-11 drain the accumulator, one row and up to 128 columns a
-//     thread, all of them in registers at once, so that the accumulator is
-//     handed back before they are converted and stored: a hidden row's block of
-//     128 columns is then a thread's own (ReLU, maximum, scale, 8 bits).
-// BN = 256 has one accumulator of 256 columns (two would leave TMEM no room
-// for the scales); its 8 drain warps take the two column halves side by side.
-// BN = 128 and 64 have two accumulators, four drain warps each.
+// One persistent kernel on CTA pairs for both products, with the weights as the
+// MMA's M and the tokens as its flexible N: a tile is 256 output features x up
+// to 256 of one expert's tokens (the expert's tokens are split evenly, in steps
+// of 16, so few columns are padding).  CTA r of a pair holds features 128 r ..
+// 128 r + 127 and loads half of the tokens.  Two accumulators share the 448
+// TMEM columns that the scales leave (acc_column).
+//   * warp 0 loads the weights and warp 2 the tokens by TMA, 256 bytes deep (two
+//     boxes in the 128-byte swizzle), through a ring of three stages;
+//   * warp 3 brings the scales of each 512 columns, laid out as tcgen05.cp wants
+//     them (row r at lane r % 32, word r / 32; both CTAs need every token's),
+//     from arrays of words [512 columns][slot] that the gather and the first
+//     product's drain write (a tile's rows are then consecutive);
+//   * warp 1 of the leader copies the scales to TMEM and issues the MMAs;
+//   * warps 4-11 drain: one feature a lane, 32 tokens at a time.  For the
+//     hidden rows a token's scale is over the CTA's 128 features, that is 32
+//     lanes of four warps: a warp maximum per token, then one exchange through
+//     shared memory.
+//
+// At these tile sizes (a 32-deep MMA takes N / 2 cycles) the issuing warps set
+// the pace as easily as the tensor core: a TMA issue takes about 200 cycles and
+// a stage of four MMAs about 510 when one lane of a divergent warp issues them,
+// 160 and 350 when the whole warp runs the loop and an elected lane issues
+// (addresses then live in uniform registers), and a stage's waits and commit
+// are another 150: hence warp-uniform loops, two loading warps, and stages of
+// eight MMAs.
 #include <cstring>
 
 #include "q8.cuh"
@@ -36,55 +47,58 @@ namespace smoe {
 namespace {
 
 constexpr int kQK = 128;                               // K block: 128 codes
-constexpr uint32_t kQABytes = 128 * kQK;               // 16 KB
-constexpr int kQThreads = 384;
-constexpr int kQDrainWarps = 8;
-constexpr int kSfSlots = 4;                            // ring of scale groups (512 columns each)
-constexpr uint32_t kSfBytes = 3 * 512;                 // rows, weight rows 0-127, 128-255
-constexpr uint32_t kSfTmem = 256;                      // TMEM columns 256 + 16 slot
-constexpr uint32_t kQStageOut = 2048;                  // per drain warp: 32 rows x 64 bytes
+constexpr int kQTok = 256;                             // most tokens of a tile
+constexpr int kQStages = 3;                            // of two K blocks
+constexpr uint32_t kQWBytes = 128 * kQK;               // 16 KB: 128 weight rows of a block
+constexpr uint32_t kQTokBytes = kQTok / 2 * kQK;       // 16 KB: up to 128 token rows
+constexpr uint32_t kQStageBytes = 2 * (kQWBytes + kQTokBytes);   // W, W, tokens, tokens
+constexpr int kQHalves = 4;                            // drain warps per lane quarter
+constexpr int kQDrainWarps = 4 * kQHalves;
+constexpr int kQThreads = 128 + 32 * kQDrainWarps;
+constexpr int kSfSlots = 6;                            // ring of scale groups (512 columns each)
+constexpr int kSfTmemSlots = 4;
+constexpr uint32_t kSfBytes = 3 * 512;                 // weight rows, tokens 0-127, 128-255
+constexpr uint32_t kSfTmem = 448;                      // TMEM columns 448 + 16 i, i < 4
+constexpr uint32_t kQStageOut = 128;                   // per drain warp: 32 tokens' 2^-e
+constexpr uint32_t kQRedBytes = kQHalves * 2 * 4 * 128;   // maxima: [half][parity][quarter][32]
+constexpr uint32_t kQBarBytes = 512;
 constexpr uint32_t kQTmemCols = 512;
-
-template <int BN>
-struct Q8Tile {
-  static constexpr int kStages = BN == 256 ? 4 : 6;
-  static constexpr uint32_t kBBytes = BN * kQK;
-  static constexpr uint32_t kStageBytes = kQABytes + kBBytes;
-  static constexpr int kAccs = BN == 256 ? 1 : 2;
-  static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kQDrainWarps * kQStageOut +
-                                    kSfSlots * kSfBytes + 512;   // + mts [N + 1]
-};
+// Limit of the last wait for copies in flight: a load takes microseconds.
+constexpr long long kDrainCycles = 40000000LL;
+constexpr uint32_t kQSmem = 1024 + kQStages * kQStageBytes + kQDrainWarps * kQStageOut +
+                            kSfSlots * kSfBytes + kQRedBytes + kQBarBytes;   // + pts, kept
 
 struct Q8Params {
-  int N, n_out, K, ntiles_n;
+  int N, n_out, K, ntiles_f;
   int64_t C;
-  int kblk;                  // scale bytes of a row: ceil(K / 128)
+  int kblk;                  // scale bytes of a weight row: ceil(K / 128)
   int nblk_w;                // weight blocks along n_out: ceil(n_out / 128)
+  int64_t slots;             // N*C
   const int* counts;
-  const uint8_t* as;         // [N*C, kblk]
+  const uint32_t* as;        // scale words of the rows [ceil(K / 512)][N*C]
   const uint8_t* ws;         // [N, nblk_w, kblk]
   uint8_t* hq;               // hidden: [N*C, n_out]
-  uint8_t* hs;               // hidden: [N*C, nblk_w]
+  uint8_t* hs;               // hidden: scale words [ceil(n_out / 512)][N*C], by bytes
   __nv_bfloat16* y;          // else: [N*C, n_out]
   DevErr* err;
   long long spin;
 };
 
-// D (+)= scaled A x scaled B^T; one thread.
-__device__ __forceinline__ void umma_q8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
-                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+// D (+)= scaled A x scaled B^T over both CTAs; one thread of the leader.
+__device__ __forceinline__ void umma_q8_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
+      " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
       " [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
       "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
 
-// 32 rows x 16 bytes of shared memory (512 consecutive bytes) to 4 TMEM columns,
-// repeated in the four lane quarters.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+// 32 rows x 16 bytes of each CTA's shared memory (512 consecutive bytes) to 4
+// columns of its TMEM, repeated in the four lane quarters.
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
                : "memory");
 }
 
@@ -106,19 +120,25 @@ __host__ __device__ constexpr uint32_t idesc_q8(int M, int N) {
 }
 __device__ __forceinline__ uint32_t idesc_byte(uint32_t b) { return (b << 4) | (b << 29); }
 
-__device__ __forceinline__ int64_t kept_q8(const Q8Params& p, int e) {
+__device__ __forceinline__ int kept_q8(const Q8Params& p, int e) {
   const int64_t c = p.counts[e];
-  return c < 0 ? 0 : (c < p.C ? c : p.C);
+  return static_cast<int>(c < 0 ? 0 : (c < p.C ? c : p.C));
 }
+__device__ __forceinline__ int token_tiles(int kept) { return (kept + kQTok - 1) / kQTok; }
 
-// Exclusive prefix of the experts' 128-row tiles, one warp.
-__device__ void tiles_prefix_warp(const Q8Params& p, int* mts) {
+// Per expert: its kept tokens, and the exclusive prefix of its tiles (token
+// tiles x feature tiles); one warp.
+__device__ void tiles_prefix_warp(const Q8Params& p, int* pts, int* kept) {
   const int lane = threadIdx.x & 31;
   const int per = (p.N + 31) / 32;
   int s = 0;
   for (int i = 0; i < per; ++i) {
     const int e = lane * per + i;
-    if (e < p.N) s += static_cast<int>((kept_q8(p, e) + 127) >> 7);
+    if (e < p.N) {
+      const int k = kept_q8(p, e);
+      kept[e] = k;
+      s += token_tiles(k) * p.ntiles_f;
+    }
   }
   int inc = s;
 #pragma unroll
@@ -130,153 +150,216 @@ __device__ void tiles_prefix_warp(const Q8Params& p, int* mts) {
   for (int i = 0; i < per; ++i) {
     const int e = lane * per + i;
     if (e < p.N) {
-      mts[e] = run;
-      run += static_cast<int>((kept_q8(p, e) + 127) >> 7);
+      pts[e] = run;
+      run += token_tiles(kept[e]) * p.ntiles_f;
     }
   }
-  if (lane == 31) mts[p.N] = inc;
+  if (lane == 31) pts[p.N] = inc;
 }
 
-// Scale bytes 4g .. 4g + 3 of a row of `kblk` bytes (past its end: 2^0).
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int g, int kblk) {
-  if ((kblk & 3) == 0) return __ldg(reinterpret_cast<const uint32_t*>(row) + g);
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int b = 4 * g + i;
-    const uint32_t v = b < kblk ? __ldg(row + b) : 127u;
-    w |= v << (8 * i);
+// First TMEM column of a tile's accumulator: even tiles grow from column 0, odd
+// ones end at the scales (column 448).  Two tiles in a row overlap where their
+// columns sum to more than 448, by 64 columns at most.
+__device__ __forceinline__ uint32_t acc_column(int acc, int nmma) {
+  return acc == 0 ? 0u : kSfTmem - static_cast<uint32_t>(nmma);
+}
+
+struct Q8TileAt {
+  int e;        // expert
+  int t0;       // first token slot of the tile within the expert
+  int nv;       // its tokens (1..256)
+  int nmma;     // the MMA's N: nv rounded up to 16
+  int f0;       // first output feature of the pair tile
+};
+
+__device__ __forceinline__ int small_div(int a, int b) {      // b is 1 or 2 most of the time
+  return b == 1 ? a : (b == 2 ? a >> 1 : a / b);
+}
+
+// Tiles in the order of a pair's walk (tile numbers that only grow).  An
+// expert's token tiles vary fastest, so pairs running side by side share the
+// weight tile.  The second product takes the list from its end: the last
+// experts' hidden rows, written last, are the ones still in L2.  The walk
+// remembers its expert: a search per tile would cost more than a short tile.
+template <bool kHidden>
+struct Q8Walk {
+  const Q8Params& p;
+  const int *pts, *kept;
+  int e;
+  __device__ __forceinline__ Q8Walk(const Q8Params& p_, const int* pts_, const int* kept_)
+      : p(p_), pts(pts_), kept(kept_), e(kHidden ? 0 : p_.N - 1) {}
+  __device__ __forceinline__ Q8TileAt at(int tile) {
+    if (!kHidden) tile = pts[p.N] - 1 - tile;
+    int steps = 0;
+    while (kHidden ? pts[e + 1] <= tile : pts[e] > tile) {
+      if (++steps > 8) {                     // far: halve the rest
+        int lo = kHidden ? e : 0, hi = kHidden ? p.N : e;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (pts[mid] <= tile) lo = mid; else hi = mid;
+        }
+        e = lo;
+        break;
+      }
+      e += kHidden ? 1 : -1;
+    }
+    Q8TileAt t;
+    t.e = e;
+    const int k = kept[e];
+    const int nt = token_tiles(k);
+    const int local = tile - pts[e];
+    const int mf = small_div(local, nt);
+    const int size = (small_div(k + nt - 1, nt) + 15) & ~15;
+    t.t0 = (local - mf * nt) * size;
+    t.nv = k - t.t0 < size ? k - t.t0 : size;
+    t.nmma = (t.nv + 15) & ~15;
+    t.f0 = mf * 256;
+    return t;
   }
-  return w;
+};
+
+// Rows of the token boxes: the smallest of eight that holds half a tile (what a
+// box brings beyond it costs shared-memory bandwidth).
+constexpr int kQBoxes = 8;
+struct Q8Maps {
+  CUtensorMap w;
+  CUtensorMap tok[kQBoxes];
+};
+__host__ __device__ constexpr uint32_t box_rows(int box) {
+  return box < 3 ? 8u << box : (box == 3 ? 64u : 16u * box + 16u);   // 8 16 32 64 80 96 112 128
+}
+__device__ __forceinline__ int box_of(int half) {
+  return half <= 8 ? 0 : (half <= 16 ? 1 : (half <= 32 ? 2 : (half <= 64 ? 3 : (half - 1) >> 4)));
 }
 
-template <int BN, bool kHidden>
-__global__ void __launch_bounds__(kQThreads, 1)
-    expert_gemm_q8_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                          const __grid_constant__ CUtensorMap tmap_b,
-                          const __grid_constant__ CUtensorMap tmap_out, Q8Params p) {
-  using L = Q8Tile<BN>;
-  constexpr int kStages = L::kStages;
-  constexpr int kAccs = L::kAccs;
+__device__ __forceinline__ void cp_async4_s(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// relu of four fp32 values as e4m3 codes, `a` in the lowest byte.
+__device__ __forceinline__ uint32_t relu_e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// Lane j: an upper bound of the values v[j] of the warp's lanes (or 0 where all
+// are below it) with the scale of their maximum.  The bound has the upper 16
+// bits of the fp32 number, rounded up: a scale changes where the significand
+// passes 1.75, a border that 16 bits hold exactly, and numbers above zero order
+// as their bits.  Two tokens share a register; five exchanges halve the tokens
+// that a lane still follows (16 shuffles; a warp reduction per token, 32 of two
+// cycles of the whole SM each, took 310-940 cycles of a chunk's drain).
+__device__ __forceinline__ float warp_token_max(const uint32_t (&v)[32], int lane) {
+  uint32_t m[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    m[i] = __vmaxs2(__byte_perm(v[2 * i] + 0xFFFFu, v[2 * i + 1] + 0xFFFFu, 0x7632), 0u);
+#pragma unroll
+  for (int n = 8; n >= 1; n >>= 1) {                 // lane bit 2 n picks the upper half
+    const bool up = (lane & (2 * n)) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const uint32_t keep = up ? m[i + n] : m[i];
+      const uint32_t send = up ? m[i] : m[i + n];
+      m[i] = __vmaxs2(keep, __shfl_xor_sync(0xffffffffu, send, 2 * n));
+    }
+  }
+  const uint32_t p = __vmaxs2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+  return __uint_as_float((lane & 1) ? p & 0xFFFF0000u : p << 16);
+}
+
+template <bool kHidden>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
+    expert_gemm_q8_kernel(const __grid_constant__ Q8Maps maps, Q8Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint8_t* stage_out = smem + kStages * L::kStageBytes;
+  uint8_t* stage_out = smem + kQStages * kQStageBytes;
   uint8_t* sf = stage_out + kQDrainWarps * kQStageOut;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sf + kSfSlots * kSfBytes);
-  uint64_t* empty = full + kStages;
-  uint64_t* sfull = empty + kStages;
-  uint64_t* sempty = sfull + kSfSlots;
-  uint64_t* tfull = sempty + kSfSlots;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
+  float* red = reinterpret_cast<float*>(sf + kSfSlots * kSfBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sf + kSfSlots * kSfBytes + kQRedBytes);
+  uint64_t* empty = full + kQStages;        // full: leader, both CTAs' bytes; empty: local
+  uint64_t* sfull = empty + kQStages;       // scales in shared memory (leader: both CTAs')
+  uint64_t* sempty = sfull + kSfSlots;      // local: copied to TMEM
+  uint64_t* tfull = sempty + kSfSlots;      // local: accumulator ready
+  uint64_t* tempty = tfull + 2;             // leader: accumulator drained
+  uint64_t* tover = tempty + 2;             // leader: the columns that the next tile may need
+  uint64_t* drain = tover + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* mts = reinterpret_cast<int*>(sf + kSfSlots * kSfBytes + 512);     // [N + 1]
+  int* pts = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + kQBarBytes);   // [N + 1]
+  int* kept = pts + p.N + 1;                                                          // [N]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cid = static_cast<int>(cluster_id_x());
+  const int ncl = static_cast<int>(cluster_count_x());
   const long long lim = p.spin;
   const int kblocks = (p.K + kQK - 1) / kQK;
 
-  if (warp == 0) tiles_prefix_warp(p, mts);
+  if (warp == 0) tiles_prefix_warp(p, pts, kept);
   if (threadIdx.x == 32) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
+    for (int s = 0; s < kQStages; ++s) {
+      mbar_init(&full[s], 2);               // the leader's two loading warps
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kSfSlots; ++s) {
-      mbar_init(&sfull[s], 1);
+      // 32 asynchronous copies' arrivals and the warp's; the leader's also takes
+      // the follower's relay
+      mbar_init(&sfull[s], leader ? 34 : 33);
       mbar_init(&sempty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], kAccs == 1 ? 256 : 128);
+      mbar_init(&tempty[b], 2 * kQDrainWarps);
+      mbar_init(&tover[b], 2 * kQDrainWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   __syncthreads();
-  const int total = mts[p.N] * p.ntiles_n;
-  if (static_cast<int>(blockIdx.x) >= total) return;     // uniform for the block
+  const int total = pts[p.N];
+  if (cid >= total) return;                 // same decision in both CTAs of the pair
   if (warp == 1) {
-    tmem_alloc(tmem_holder, kQTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(tmem_holder, kQTmemCols);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                           // the peer's barriers exist before any remote use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  const uint32_t full_lead = map_to_rank(smem_u32(full), 0);
+  const uint32_t sfull_lead = map_to_rank(smem_u32(sfull), 0);
+  const uint32_t tempty_lead = map_to_rank(smem_u32(tempty), 0);
+  const uint32_t tover_lead = map_to_rank(smem_u32(tover), 0);
 
-  if (warp == 0) {
-    // ------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tmap_a);
-      tma_prefetch_desc(&tmap_b);
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t issued_mask = 0, issued_phase = 0;
-      for (int tile = blockIdx.x; tile < total && !*abort_flag; tile += gridDim.x) {
-        int e, m, n;
-        decode_tile(tile, mts, p.N, p.ntiles_n, e, m, n);
-        const int row = static_cast<int>(static_cast<int64_t>(e) * p.C + m * 128);
-        bool ok = true;
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, lim)) {
-            report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmProducer, tile);
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          uint8_t* sa = smem + stage * L::kStageBytes;
-          mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
-          tma_load_2d(sa, &tmap_a, &full[stage], kb * kQK, row);
-          tma_load_3d(sa + kQABytes, &tmap_b, &full[stage], kb * kQK, n * BN, e);
-          issued_mask |= 1u << stage;
-          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
-        }
-        if (!ok) break;
-      }
-      // Never leave with copies in flight into this CTA's shared memory.
-      for (int s = 0; s < kStages; ++s)
-        if (((issued_mask >> s) & 1u) &&
-            !mbar_wait(&full[s], (issued_phase >> s) & 1u, kDefaultSpinCycles))
-          report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereDrain, s);
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------- scales
-    int slot = 0;
+  Q8Walk<kHidden> walk(p, pts, kept);
+  const int kstages = (kblocks + 1) / 2;
+  if (warp == 0 || warp == 2) {
+    // ------------------------------ TMA: warp 0 the weights, warp 2 the tokens
+    const bool tokens = warp == 2;
+    if (elect_one()) tma_prefetch_desc(tokens ? &maps.tok[kQBoxes - 1] : &maps.w);
+    int stage = 0;
     uint32_t phase = 0;
-    const int groups = (kblocks + 3) / 4;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-      if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
-      int e, m, n;
-      decode_tile(tile, mts, p.N, p.ntiles_n, e, m, n);
-      const int64_t kept = kept_q8(p, e);
-      const uint8_t* arow[4];
-      bool aon[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t r = static_cast<int64_t>(m) * 128 + 32 * j + lane;
-        aon[j] = r < kept;
-        arow[j] = p.as + (static_cast<int64_t>(e) * p.C + (aon[j] ? r : 0)) * p.kblk;
-      }
-      const int b0 = n * BN / 128;
-      const int b1 = b0 + 1 < p.nblk_w ? b0 + 1 : p.nblk_w - 1;
-      const uint8_t* w0 = p.ws + (static_cast<int64_t>(e) * p.nblk_w + b0) * p.kblk;
-      const uint8_t* w1 = p.ws + (static_cast<int64_t>(e) * p.nblk_w + b1) * p.kblk;
+    uint32_t issued_mask = 0, issued_phase = 0;
+    for (int tile = cid; tile < total; tile += ncl) {
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      const Q8TileAt t = walk.at(tile);
+      const int half = t.nmma >> 1;
+      const int box = box_of(half);
+      const CUtensorMap* map = tokens ? &maps.tok[box] : &maps.w;
+      const int row = tokens ? static_cast<int>(static_cast<int64_t>(t.e) * p.C + t.t0 +
+                                                static_cast<int>(rank) * half)
+                             : t.f0 + static_cast<int>(rank) * 128;
+      const uint32_t bytes = tokens ? box_rows(box) * kQK : kQWBytes;
+      const uint32_t step = tokens ? kQTokBytes : kQWBytes;
       bool ok = true;
-      for (int g = 0; g < groups; ++g) {
-        uint32_t a[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = aon[j] ? scale_word(arow[j], g, p.kblk) : 0x7F7F7F7Fu;
-        const uint32_t u0 = scale_word(w0, g, p.kblk);
-        const uint32_t u1 = BN > 128 ? scale_word(w1, g, p.kblk) : 0u;
-        int w_ok = 1;
-        if (lane == 0) w_ok = mbar_wait(&sempty[slot], phase ^ 1u, lim) ? 1 : 0;
-        w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
-        if (!w_ok) {
+      for (int ks = 0; ks < kstages; ++ks) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, lim))) {
           if (lane == 0) {
             report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmProducer, tile);
             *abort_flag = 1;
@@ -284,214 +367,332 @@ __global__ void __launch_bounds__(kQThreads, 1)
           ok = false;
           break;
         }
-        const uint32_t dst = smem_u32(sf + slot * kSfBytes) + lane * 16;
-        st_shared_v4u(dst, a[0], a[1], a[2], a[3]);
-        st_shared_v4u(dst + 512, u0, u0, u0, u0);
-        if (BN > 128) st_shared_v4u(dst + 1024, u1, u1, u1, u1);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[slot]);
-        if (++slot == kSfSlots) { slot = 0; phase ^= 1u; }
+        const int nb = kblocks - 2 * ks < 2 ? 1 : 2;
+        uint8_t* dst = smem + stage * kQStageBytes + (tokens ? 2 * kQWBytes : 0u);
+        const uint32_t bar = full_lead + 8u * stage;
+        if (elect_one()) {
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2u * nb * bytes);
+          if (tokens) {
+            tma_load_2d_pair(dst, map, bar, 2 * ks * kQK, row);
+            if (nb == 2) tma_load_2d_pair(dst + step, map, bar, (2 * ks + 1) * kQK, row);
+          } else {
+            tma_load_3d_pair(dst, map, bar, 2 * ks * kQK, row, t.e);
+            if (nb == 2) tma_load_3d_pair(dst + step, map, bar, (2 * ks + 1) * kQK, row, t.e);
+          }
+        }
+        issued_mask |= 1u << stage;
+        issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == kQStages) { stage = 0; phase ^= 1u; }
       }
       if (!ok) break;
     }
+    // Both CTAs' bytes land on the leader's barriers: the leader waits for
+    // every issued stage before the final cluster barrier.  (A stage that only
+    // one of the two warps had issued before a failure does not complete: its
+    // bytes are then waited for by the limit alone.)
+    if (leader && lane == 0) {
+      for (int s = 0; s < kQStages; ++s)
+        if (((issued_mask >> s) & 1u) &&
+            !mbar_wait_cluster(&full[s], (issued_phase >> s) & 1u, kDrainCycles))
+          report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereDrain, s);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------- scales
+    // Groups of 512 columns by asynchronous copies, as far ahead as the ring
+    // goes (a group is consumed in about the time that one load takes).  The
+    // copies arrive on the group's barrier by themselves; the proxy fence between
+    // them and tcgen05.cp is left to warps with no copies of their own in flight,
+    // since it waits for all of a thread's.
+    const int groups = (kblocks + 3) / 4;
+    const bool words = (p.kblk & 3) == 0;
+    int tile = cid, g = 0;
+    Q8TileAt t{};
+    const uint8_t* wrow = nullptr;
+    auto enter = [&]() {
+      t = walk.at(tile);
+      int b = (t.f0 >> 7) + static_cast<int>(rank);
+      if (b >= p.nblk_w) b = p.nblk_w - 1;             // features past the end: zero rows
+      wrow = p.ws + (static_cast<int64_t>(t.e) * p.nblk_w + b) * p.kblk;
+    };
+    int slot = 0;
+    uint32_t phase = 0;
+    enter();
+    while (tile < total) {
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sempty[slot], phase ^ 1u, lim))) {
+        if (lane == 0) {
+          report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmProducer, tile);
+          *abort_flag = 1;
+        }
+        break;
+      }
+      const uint32_t dst = smem_u32(sf + slot * kSfBytes) + lane * 16;
+      const uint32_t* src =
+          p.as + static_cast<int64_t>(g) * p.slots + static_cast<int64_t>(t.e) * p.C + t.t0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {                    // rows past the last: any scale
+        const int r = 32 * j + lane;
+        cp_async4_s(dst + 512 + (j >> 2) * 512 + (j & 3) * 4, src + (r < t.nv ? r : 0));
+      }
+      // the weight rows' word, four times a lane; by plain loads where it is not
+      // aligned (bytes past the row's end: its last one)
+      if (words) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cp_async4_s(dst + j * 4, wrow + 4 * g);
+        cp_async_mbar_arrive_noinc(&sfull[slot]);
+        if (lane == 0) mbar_arrive_relaxed(&sfull[slot]);
+      } else {
+        cp_async_mbar_arrive_noinc(&sfull[slot]);
+        const int b0 = 4 * g, left = p.kblk - b0;
+        uint32_t u = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          u |= static_cast<uint32_t>(__ldg(wrow + b0 + (k < left ? k : left - 1))) << (8 * k);
+        st_shared_v4u(dst, u, u, u, u);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfull[slot]);
+      }
+      if (++slot == kSfSlots) { slot = 0; phase ^= 1u; }
+      if (++g == groups) {
+        g = 0;
+        tile += ncl;
+        if (tile < total) enter();
+      }
+    }
+    cp_async_wait_all();                               // none in flight behind this
   } else if (warp == 1) {
-    // --------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_q8(128, BN);
-      int stage = 0, slot = 0;
+    // ------------------------------------------------- MMA issuer (leader)
+    if (leader) {
+      int stage = 0, slot = 0, tslot = 0;
       uint32_t phase = 0, sphase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       uint32_t sfa = 0;
+      int last_nmma = 0;
       bool any = false;
-      for (int tile = blockIdx.x; tile < total && !*abort_flag; tile += gridDim.x) {
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, lim)) {
-          report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmMma, tile);
-          *abort_flag = 1;
-          break;
-        }
+      const uint32_t smem0 = smem_u32(smem), sf0 = smem_u32(sf);
+      for (int tile = cid; tile < total; tile += ncl) {
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+        const int nmma = walk.at(tile).nmma;
+        const uint32_t idesc = idesc_q8(256, nmma);
+        bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, lim));
+        // columns that the last tile has too: its drain takes those first
+        if (ok && nmma + last_nmma > static_cast<int>(kSfTmem))
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_cluster(&tover[acc ^ 1], acc == 0 ? acc_phase ^ 1u : acc_phase, lim));
+        last_nmma = nmma;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-        bool ok = true;
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if ((kb & 3) == 0) {
-            if (!mbar_wait(&sfull[slot], sphase, lim)) {
-              ok = false;
-            } else {
-              tc_fence_after();
-              sfa = tmem_base + kSfTmem + 16u * slot;
-              const uint32_t src = smem_u32(sf + slot * kSfBytes);
-              tmem_cp_scales(sfa, scales_desc(src));
-              tmem_cp_scales(sfa + 4, scales_desc(src + 512));
-              if (BN > 128) tmem_cp_scales(sfa + 8, scales_desc(src + 1024));
-              any = true;
-              umma_commit(&sempty[slot]);
-              if (++slot == kSfSlots) { slot = 0; sphase ^= 1u; }
+        const uint32_t d_tmem = tmem_base + acc_column(acc, nmma);
+        for (int ks = 0; ok && ks < kstages; ++ks) {
+          if ((ks & 1) == 0) {                         // the scales of the next 4 K blocks
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sfull[slot], sphase, lim));
+            if (!ok) break;
+            fence_proxy_async_smem();                  // this CTA's scales -> tcgen05.cp
+            tc_fence_after();
+            sfa = tmem_base + kSfTmem + 16u * tslot;
+            tslot = (tslot + 1) % kSfTmemSlots;   // (copies and MMAs run in order)
+            const uint32_t src = sf0 + slot * kSfBytes;
+            if (elect_one()) {
+              tmem_cp_scales_pair(sfa, scales_desc(src));
+              tmem_cp_scales_pair(sfa + 4, scales_desc(src + 512));
+              if (nmma > 128) tmem_cp_scales_pair(sfa + 8, scales_desc(src + 1024));
+              umma_commit_pair(&sempty[slot], 0x3);
             }
+            any = true;
+            if (++slot == kSfSlots) { slot = 0; sphase ^= 1u; }
           }
-          if (!ok || !mbar_wait(&full[stage], phase, lim)) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, lim));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t wd = sw128_kmajor_desc(smem0 + stage * kQStageBytes);
+          const uint64_t td = sw128_kmajor_desc(smem0 + stage * kQStageBytes + 2 * kQWBytes);
+          const uint32_t id = idesc | idesc_byte(2u * (ks & 1));
+          if (elect_one()) {
+            // descriptors count 16 bytes: a 32-deep step is 2 of them
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_q8_pair(d_tmem, wd + 2 * k, td + 2 * k, id, sfa, sfa + 4, (ks | k) != 0 ? 1u : 0u);
+            if (2 * ks + 1 < kblocks) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_q8_pair(d_tmem, wd + (kQWBytes >> 4) + 2 * k, td + (kQTokBytes >> 4) + 2 * k,
+                             id + idesc_byte(1), sfa, sfa + 4, 1u);
+            }
+            umma_commit_pair(&empty[stage], 0x3);
+          }
+          any = true;
+          if (++stage == kQStages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) {
+          if (lane == 0) {
             report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmMma, tile);
             *abort_flag = 1;
-            ok = false;
+          }
+          break;
+        }
+        if (elect_one()) umma_commit_pair(&tfull[acc], 0x3);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      __syncwarp();
+      if (any && __any_sync(0xffffffffu, *abort_flag)) {
+        if (elect_one()) umma_commit_pair(drain, 0x1);
+        if (!__all_sync(0xffffffffu, mbar_wait(drain, 0, kDefaultSpinCycles)) && lane == 0)
+          report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereDrain, -1);
+      }
+    } else {
+      // -------------------------- follower: relay its scales to the leader
+      const int groups = (kblocks + 3) / 4;
+      int slot = 0;
+      uint32_t phase = 0;
+      for (int tile = cid; tile < total; tile += ncl) {
+        bool ok = !__any_sync(0xffffffffu, *abort_flag);
+        for (int g = 0; ok && g < groups; ++g) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&sfull[slot], phase, lim));
+          if (!ok) {
+            if (lane == 0) {
+              report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmProducer, tile);
+              *abort_flag = 1;
+            }
             break;
           }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * L::kStageBytes);
-          const uint32_t sb = sa + kQABytes;
-          const uint32_t id = idesc | idesc_byte(static_cast<uint32_t>(kb & 3));
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_q8(d_tmem, sw128_kmajor_desc(sa + k * 32), sw128_kmajor_desc(sb + k * 32), id, sfa,
-                    sfa + 4, (kb | k) != 0 ? 1u : 0u);
-          any = true;
-          umma_commit(&empty[stage]);
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(sfull_lead + 8u * slot);
+          if (++slot == kSfSlots) { slot = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        umma_commit(&tfull[acc]);
-        if (++acc == kAccs) { acc = 0; acc_phase ^= 1u; }
-      }
-      if (any && *abort_flag) {
-        umma_commit(drain);
-        if (!mbar_wait(drain, 0, kDefaultSpinCycles))
-          report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereDrain, -1);
       }
     }
   } else if (warp >= 4) {
     // --------------------------------------------------------- drain warps
-    constexpr int kCols = BN < 128 ? BN : 128;            // columns of a thread
+    // Quarter q of the CTA's 128 features (one a lane); the kQHalves warps of a
+    // quarter take the chunks of 32 tokens in turn, first those whose columns the
+    // next tile may need.
     const int q = warp & 3;
-    const int half = (warp - 4) >> 2;                     // column half, or accumulator
-    const uint32_t stg = smem_u32(stage_out + (warp - 4) * kQStageOut);
-    const uint32_t swz = static_cast<uint32_t>((lane >> 1) & 3);
-    if (lane == 0) tma_prefetch_desc(&tmap_out);
-    const int acc = kAccs == 1 ? 0 : half;
+    const int h = (warp - 4) >> 2;
+    float* isv = reinterpret_cast<float*>(stage_out) + (warp - 4) * 32;   // tokens' 2^-e
+    float* redh = red + h * 256;                       // [parity][quarter][32]
+    int acc = 0, par = 0;
     uint32_t acc_phase = 0;
-    int turn = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-      if (kAccs == 2 && (turn++ & 1) != half) continue;   // the other accumulator's tile
+    // relaxed: only TMEM loads, which have been waited for, are handed over (a
+    // release would hold the warp until its rows' stores had reached memory)
+    auto arrive_lead = [&](uint64_t* bar, uint32_t lead, int b) {
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive_relaxed(&bar[b]);
+        else mbar_arrive_remote_relaxed(lead + 8u * b);
+      }
+    };
+    for (int tile = cid; tile < total; tile += ncl) {
       const bool ok = __all_sync(0xffffffffu, mbar_wait_sleepy(&tfull[acc], acc_phase, lim));
-      if (!ok) {
+      // The four warps of a half meet at a barrier for each hidden chunk: they
+      // go on, or leave, together.
+      if (kHidden) {
+        int all_ok;
+        asm volatile(
+            "{\n .reg .pred p, r;\n setp.ne.b32 p, %1, 0;\n"
+            " barrier.cta.red.and.pred r, %2, 128, p;\n selp.u32 %0, 1, 0, r;\n}\n"
+            : "=r"(all_ok)
+            : "r"(ok ? 1 : 0), "r"(1 + h)
+            : "memory");
+        if (!all_ok) {
+          if (lane == 0) {
+            report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmEpilogue, tile);
+            *abort_flag = 1;
+          }
+          break;
+        }
+      } else if (!ok) {
         if (lane == 0) {
           report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmEpilogue, tile);
           *abort_flag = 1;
         }
         break;
       }
-      acc_phase ^= 1u;
       tc_fence_after();
-      int e, m, n;
-      decode_tile(tile, mts, p.N, p.ntiles_n, e, m, n);
-      const int64_t kept = kept_q8(p, e);
-      const int64_t rbase = static_cast<int64_t>(m) * 128 + q * 32;
-      const int col0 = n * BN + (kAccs == 1 ? half * 128 : 0);
-      const int left = p.n_out - col0;
-      const int ncols = left < kCols ? left : kCols;      // 64, 128, or none
-      const bool work = rbase < kept && ncols > 0;        // warp-uniform
+      const Q8TileAt t = walk.at(tile);
+      const int fc = t.f0 + static_cast<int>(rank) * 128;          // the CTA's first feature
+      const int fb = fc + q * 32;                                  // the warp's
+      const bool on = fb < p.n_out;                                // warp-uniform
+      const int nch = (t.nv + 31) >> 5;
+      const int64_t row0 = static_cast<int64_t>(t.e) * p.C + t.t0;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                             static_cast<uint32_t>(kAccs == 1 ? half * 128 : acc * BN);
-      // hidden: the values, after the ReLU; else packed bf16 pairs
-      float f[kHidden ? kCols : 1];
-      uint32_t pk[kHidden ? kCols / 4 : kCols / 2];
-      if (work) {
+                             acc_column(acc, t.nmma);
+      if (h >= 2 || h >= nch) arrive_lead(tover, tover_lead, acc);   // none of those
+      for (int i = h; i < nch; i += kQHalves) {
+        const int c = acc == 0 ? nch - 1 - i : i;
+        uint32_t v[32];
+        tmem_ld32_issue(taddr + static_cast<uint32_t>(c * 32), v);
+        tmem_ld_wait(v);
+        if (i < 2) {                                               // at most 64 columns overlap
+          tc_fence_before();
+          arrive_lead(tover, tover_lead, acc);
+        }
+        const int j0 = c * 32;
+        const int jn = t.nv - j0 < 32 ? t.nv - j0 : 32;            // tokens of the chunk
+        if (kHidden) {
+          const float mine = warp_token_max(v, lane);
+          float* r = redh + par * 128;
+          par ^= 1;
+          r[q * 32 + lane] = mine;
+          named_bar_sync(1 + h, 128);
+          const float a = fmaxf(fmaxf(r[lane], r[32 + lane]), fmaxf(r[64 + lane], r[96 + lane]));
+          const int ex = q8_exponent(a);
+          if (!on) continue;                           // (no shared memory touched yet)
+          // the token's 2^-e to every lane
+          __syncwarp();                                // the last chunk's are read
+          isv[lane] = q8_inv_scale(ex);
+          __syncwarp();
+          float4 sc[8];
 #pragma unroll
-        for (int c = 0; c < kCols / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld32_issue(taddr + c * 32, v);
-          tmem_ld_wait(v);
-          if (kHidden) {
+          for (int k = 0; k < 8; ++k) sc[k] = reinterpret_cast<const float4*>(isv)[k];
+          // codes of tokens 4k .. 4k + 3 of this feature in a word; a transpose of
+          // four lanes' words makes it four features of token 4k + lane % 4, and a
+          // store writes 4 tokens x 32 bytes
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              f[kHidden ? 32 * c + j : 0] = fmaxf(__uint_as_float(v[j]), 0.f);
-          } else {
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t w = relu_e4m3x4(
+                __uint_as_float(v[4 * k]) * sc[k].x, __uint_as_float(v[4 * k + 1]) * sc[k].y,
+                __uint_as_float(v[4 * k + 2]) * sc[k].z, __uint_as_float(v[4 * k + 3]) * sc[k].w);
+            const uint32_t t1 = __shfl_xor_sync(0xffffffffu, w, 1);
+            const uint32_t x = (lane & 1) ? __byte_perm(t1, w, 0x7351) : __byte_perm(w, t1, 0x6240);
+            const uint32_t t2 = __shfl_xor_sync(0xffffffffu, x, 2);
+            const uint32_t z = (lane & 2) ? __byte_perm(t2, x, 0x7632) : __byte_perm(x, t2, 0x5410);
+            const int rr = 4 * k + (lane & 3);
+            if (rr < jn)
+              *reinterpret_cast<uint32_t*>(p.hq + (row0 + j0 + rr) * p.n_out + fb + (lane & ~3)) = z;
+          }
+          if (q == 0 && lane < jn)
+            p.hs[(static_cast<int64_t>(fc >> 9) * p.slots + row0 + j0 + lane) * 4 + ((fc >> 7) & 3)] =
+                static_cast<uint8_t>(q8_scale_byte(ex));
+        } else if (on) {
+          // tokens j and j + 1 of this feature in a word; exchanged with the next
+          // lane it is two features of one token, and a store writes 2 tokens x 64
+          // bytes
+          __nv_bfloat16* dst = p.y + (row0 + j0 + (lane & 1)) * p.n_out + fb + (lane & ~1);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              pk[16 * c + j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+          for (int j = 0; j < 32; j += 2) {
+            const uint32_t w = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, w, 1);
+            const uint32_t z = (lane & 1) ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+            if (j + (lane & 1) < jn)
+              *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * p.n_out) = z;
           }
         }
       }
       tc_fence_before();
-      mbar_arrive(&tempty[acc]);
-      if (!work) continue;
-      const int64_t row = static_cast<int64_t>(e) * p.C + rbase + lane;
-      const bool valid = rbase + lane < kept;
-      const bool bulk = rbase + 32 <= kept;
-      if (kHidden) {
-        float a = 0.f;
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-          if (j >= 64 && ncols <= 64) f[kHidden ? j : 0] = 0.f;     // past the last column
-          a = fmaxf(a, f[kHidden ? j : 0]);
-        }
-        const int ex = q8_exponent(a);
-        const float is = q8_inv_scale(ex);
-#pragma unroll
-        for (int j = 0; j < kCols / 4; ++j) {
-          const float* g = f + (kHidden ? 4 * j : 0);
-          pk[j] = kHidden ? pack_e4m3x4(g[0] * is, g[1] * is, g[2] * is, g[3] * is) : 0u;
-        }
-        if (valid) p.hs[row * p.nblk_w + col0 / 128] = static_cast<uint8_t>(q8_scale_byte(ex));
-        if (bulk) {
-#pragma unroll
-          for (int b = 0; b < kCols / 64; ++b) {
-            if (b * 64 >= ncols) break;
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              st_shared_v4u(stg + lane * 64 + ((static_cast<uint32_t>(k) ^ swz) << 4),
-                            pk[16 * b + 4 * k], pk[16 * b + 4 * k + 1], pk[16 * b + 4 * k + 2],
-                            pk[16 * b + 4 * k + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&tmap_out, stg, col0 + b * 64, static_cast<int>(row));
-              bulk_commit();
-            }
-          }
-        } else if (valid) {
-          uint4* dst = reinterpret_cast<uint4*>(p.hq + row * p.n_out + col0);
-#pragma unroll
-          for (int k = 0; k < kCols / 16; ++k)
-            if (k * 16 < ncols)
-              dst[k] = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
-        }
-      } else {
-        if (bulk) {
-#pragma unroll
-          for (int b = 0; b < kCols / 32; ++b) {
-            if (b * 32 >= ncols) break;
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              st_shared_v4u(stg + lane * 64 + ((static_cast<uint32_t>(k) ^ swz) << 4),
-                            pk[16 * b + 4 * k], pk[16 * b + 4 * k + 1], pk[16 * b + 4 * k + 2],
-                            pk[16 * b + 4 * k + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&tmap_out, stg, col0 + b * 32, static_cast<int>(row));
-              bulk_commit();
-            }
-          }
-        } else if (valid) {
-          uint4* dst = reinterpret_cast<uint4*>(p.y + row * p.n_out + col0);
-#pragma unroll
-          for (int k = 0; k < kCols / 8; ++k)
-            if (k * 8 < ncols)
-              dst[k] = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
-        }
-      }
+      arrive_lead(tempty, tempty_lead, acc);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
     }
-    if (lane == 0) bulk_wait_all();        // boxes stored from shared memory are written
   }
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                          // no CTA leaves while its peer may still signal it
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, kQTmemCols);
+  if (warp == 1) tmem_dealloc_pair(tmem_base, kQTmemCols);
 }
 
 // ------------------------------------------------------------------- host
@@ -507,97 +708,72 @@ bool encode_u8(CUtensorMap* map, const void* base, int rank, const cuuint64_t* d
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of one product: [rows, K] codes, boxes of 128 rows x 128 codes.
-bool map_rows(CUtensorMap* m, const void* base, int64_t rows, int K) {
+// Rows of one product [rows, K]: boxes of `box` rows x 128 codes.
+bool map_rows(CUtensorMap* m, const void* base, int64_t rows, int K, uint32_t box) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-  const cuuint32_t box[2] = {kQK, 128};
-  return encode_u8(m, base, 2, dims, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  const cuuint32_t b[2] = {kQK, box};
+  return encode_u8(m, base, 2, dims, b, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// Weights [N][n_out][K]: boxes of bn rows x 128 codes of one expert (zeros
+// Weights [N][n_out][K]: boxes of 128 rows x 128 codes of one expert (zeros
 // past its last row).
-bool map_weights(CUtensorMap* m, const void* base, int N, int n_out, int K, int bn) {
+bool map_weights(CUtensorMap* m, const void* base, int N, int n_out, int K) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(n_out),
                               static_cast<cuuint64_t>(N)};
-  const cuuint32_t box[3] = {kQK, static_cast<cuuint32_t>(bn), 1};
-  return encode_u8(m, base, 3, dims, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  const cuuint32_t b[3] = {kQK, 128, 1};
+  return encode_u8(m, base, 3, dims, b, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// Hidden rows as the first product's output: boxes of 32 rows x 64 codes.
-bool map_hidden_out(CUtensorMap* m, const void* base, int64_t rows, int F) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(F), static_cast<cuuint64_t>(rows)};
-  const cuuint32_t box[2] = {64, 32};
-  return encode_u8(m, base, 2, dims, box, CU_TENSOR_MAP_SWIZZLE_64B);
-}
-
-template <int BN, bool kHidden>
-cudaError_t run_q8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to,
-                   const Q8Params& p, int num_sms, cudaStream_t st) {
-  const size_t smem = Q8Tile<BN>::kSmem + sizeof(int) * (p.N + 1);
+template <bool kHidden>
+cudaError_t run_q8(const void* rows, const void* weights, const Q8Params& p, int num_sms,
+                   cudaStream_t st) {
+  const int64_t slots = static_cast<int64_t>(p.N) * p.C;
+  Q8Maps maps;
+  bool ok = map_weights(&maps.w, weights, p.N, p.n_out, p.K);
+  for (int i = 0; i < kQBoxes; ++i)
+    ok = ok && map_rows(&maps.tok[i], rows, slots, p.K, box_rows(i));
+  if (!ok) return cudaErrorInvalidValue;
+  const size_t smem = kQSmem + sizeof(int) * (2 * p.N + 1);
   static size_t smem_set[64] = {};
   cudaError_t e = ensure_smem_limit(
-      reinterpret_cast<const void*>(&expert_gemm_q8_kernel<BN, kHidden>), smem, smem_set);
+      reinterpret_cast<const void*>(&expert_gemm_q8_kernel<kHidden>), smem, smem_set);
   if (e != cudaSuccess) return e;
-  expert_gemm_q8_kernel<BN, kHidden><<<num_sms, kQThreads, smem, st>>>(ta, tb, to, p);
+  expert_gemm_q8_kernel<kHidden>
+      <<<(num_sms / 2) * 2, kQThreads, smem, st>>>(maps, p);
   return cudaGetLastError();
-}
-
-// Columns of a tile: 256 (each weight byte feeds 128 rows, each row byte 256
-// columns) unless that gives fewer tiles than SMs, when narrower tiles spread
-// the weights' reads over more of them.
-int tile_columns(int64_t mtiles, int n_out, int num_sms, int least) {
-  int bn = 256;
-  while (bn > least && mtiles * ((n_out + bn - 1) / bn) < num_sms) bn /= 2;
-  return bn;
 }
 
 }  // namespace
 
 cudaError_t launch_expert_ffn_q8(const FfnQ8Args& a, cudaStream_t st) {
   const int64_t slots = static_cast<int64_t>(a.N) * a.C;
-  // most row tiles that the batch can fill (the counts are on the device)
-  const int64_t per_expert = static_cast<int64_t>(a.N) * ((a.C + 127) / 128);
-  const int64_t mtiles = a.A < per_expert ? a.A : per_expert;
-  const int bn1 = tile_columns(mtiles, a.F, a.num_sms, 128);
-  const int bn2 = tile_columns(mtiles, a.d, a.num_sms, 64);
-  CUtensorMap ta1, tb1, to1, ta2, tb2, to2;
-  bool ok = map_rows(&ta1, a.xq, slots, a.d);
-  ok = ok && map_weights(&tb1, a.w1q, a.N, a.F, a.d, bn1);
-  ok = ok && map_hidden_out(&to1, a.hq, slots, a.F);
-  ok = ok && map_rows(&ta2, a.hq, slots, a.F);
-  ok = ok && map_weights(&tb2, a.w2q, a.N, a.d, a.F, bn2);
-  ok = ok && make_tmap_bf16_2d(&to2, a.y, a.d, slots, 32, 32, true);
-  if (!ok) return cudaErrorInvalidValue;
-
   Q8Params p{};
   p.N = a.N;
   p.n_out = a.F;
   p.K = a.d;
-  p.ntiles_n = (a.F + bn1 - 1) / bn1;
+  p.ntiles_f = (a.F + 255) / 256;
   p.C = a.C;
   p.kblk = static_cast<int>(q8_blocks(a.d));
   p.nblk_w = static_cast<int>(q8_blocks(a.F));
   p.counts = a.counts;
-  p.as = a.xs;
+  p.slots = slots;
+  p.as = a.xw;
   p.ws = a.w1s;
   p.hq = a.hq;
-  p.hs = a.hs;
+  p.hs = reinterpret_cast<uint8_t*>(a.hw);
   p.err = a.err;
   p.spin = a.spin;
-  cudaError_t e = bn1 == 256 ? run_q8<256, true>(ta1, tb1, to1, p, a.num_sms, st)
-                             : run_q8<128, true>(ta1, tb1, to1, p, a.num_sms, st);
+  cudaError_t e = run_q8<true>(a.xq, a.w1q, p, a.num_sms, st);
   if (e != cudaSuccess) return e;
   p.n_out = a.d;
   p.K = a.F;
-  p.ntiles_n = (a.d + bn2 - 1) / bn2;
+  p.ntiles_f = (a.d + 255) / 256;
   p.kblk = static_cast<int>(q8_blocks(a.F));
   p.nblk_w = static_cast<int>(q8_blocks(a.d));
-  p.as = a.hs;
+  p.as = a.hw;
   p.ws = a.w2s;
   p.hq = nullptr;
   p.hs = nullptr;
   p.y = static_cast<__nv_bfloat16*>(a.y);
-  if (bn2 == 256) return run_q8<256, false>(ta2, tb2, to2, p, a.num_sms, st);
-  if (bn2 == 128) return run_q8<128, false>(ta2, tb2, to2, p, a.num_sms, st);
-  return run_q8<64, false>(ta2, tb2, to2, p, a.num_sms, st);
+  return run_q8<false>(a.hq, a.w2q, p, a.num_sms, st);
 }
 
 }  // namespace smoe

@@ -140,12 +140,14 @@ cudaError_t launch_unpack_rows(int64_t rows, int cols, const uint8_t* q, const u
 // dst[s] = src[s] for kept slots, zeros up to the next multiple of 64 rows.
 cudaError_t launch_copy_kept_rows(int64_t rows, int cols, const void* src, const int* counts,
                                   int64_t C, void* dst, cudaStream_t st);
-// 8-bit rows and their scales into the slots of their experts (kept slots
-// only).
+// 8-bit rows into the slots of their experts (kept slots only; q null: the
+// rows are there already, xq and xs are the slots'), their scales as words
+// xw [ceil(cols / 512)][slots] (four blocks' bytes, 2^0 past the row's end),
+// and the bytes of hw [ceil(hcols / 512)][slots] past hcols' blocks as 2^0.
 cudaError_t launch_gather_rows_q8(int64_t slots, int cols, const int* slot_token,
                                   const uint8_t* xq, const uint8_t* xs, const int* counts,
-                                  int64_t C, int64_t T, uint8_t* q, uint8_t* s, DevErr* err,
-                                  cudaStream_t st);
+                                  int64_t C, int64_t T, uint8_t* q, uint32_t* xw, int hcols,
+                                  uint32_t* hw, DevErr* err, cudaStream_t st);
 // Weights [n, rows, cols] bf16 to e4m3 with a scale for each 128 x 128 block.
 cudaError_t launch_quantize_weights(int64_t n, int rows, int cols, const void* w, uint8_t* q,
                                     uint8_t* s, cudaStream_t st);
@@ -156,11 +158,11 @@ struct FfnQ8Args {
   int d, F, N;
   int64_t C;
   const uint8_t* xq;         // [N*C, d]
-  const uint8_t* xs;         // [N*C, ceil(d / 128)]
+  const uint32_t* xw;        // scale words of its rows [ceil(d / 512)][N*C]
   const int* counts;
   const uint8_t *w1q, *w1s, *w2q, *w2s;
   uint8_t* hq;               // [N*C, F] scratch
-  uint8_t* hs;               // [N*C, ceil(F / 128)] scratch
+  uint32_t* hw;              // scale words [ceil(F / 512)][N*C] scratch
   void* y;                   // [N*C, d] bf16
   DevErr* err;
   long long spin;

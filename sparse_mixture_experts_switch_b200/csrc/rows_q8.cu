@@ -116,20 +116,37 @@ __global__ void __launch_bounds__(kThreads) copy_kept_rows_kernel(
 __global__ void __launch_bounds__(kThreads) gather_rows_q8_kernel(
     int64_t slots, int cols, const int* __restrict__ slot_token, const uint8_t* __restrict__ xq,
     const uint8_t* __restrict__ xs, const int* __restrict__ counts, int64_t C, int64_t T,
-    uint8_t* __restrict__ q, uint8_t* __restrict__ s, DevErr* err) {
+    uint8_t* __restrict__ q, uint32_t* __restrict__ xw, int hcols, uint32_t* __restrict__ hw,
+    DevErr* err) {
   const int lane = threadIdx.x & 31;
   const int nv = cols / 16;
   const int nblk = static_cast<int>(q8_blocks(cols));
+  const int hblk = static_cast<int>(q8_blocks(hcols));
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < slots;
        r += step) {
     const int64_t e = r / C;
     if (r - e * C >= kept_of(counts, C, e)) continue;
-    const int64_t t = slot_row(slot_token, r, T, err);
-    const uint4* row = reinterpret_cast<const uint4*>(xq + t * cols);
-    uint4* dst = reinterpret_cast<uint4*>(q + r * cols);
-    for (int v = lane; v < nv; v += 32) dst[v] = t >= 0 ? __ldg(row + v) : make_uint4(0, 0, 0, 0);
-    for (int v = lane; v < nblk; v += 32) s[r * nblk + v] = t >= 0 ? __ldg(xs + t * nblk + v) : 127;
+    int64_t t = r;
+    if (q != nullptr) {
+      t = slot_row(slot_token, r, T, err);
+      const uint4* row = reinterpret_cast<const uint4*>(xq + t * cols);
+      uint4* dst = reinterpret_cast<uint4*>(q + r * cols);
+      for (int v = lane; v < nv; v += 32) dst[v] = t >= 0 ? __ldg(row + v) : make_uint4(0, 0, 0, 0);
+    }
+    for (int g = lane; g * 4 < nblk; g += 32) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = 4 * g + i;
+        const uint32_t v = (t >= 0 && b < nblk) ? __ldg(xs + t * nblk + b) : 127u;
+        w |= v << (8 * i);
+      }
+      xw[static_cast<int64_t>(g) * slots + r] = w;
+    }
+    // the first product's drain writes hw's bytes one by one: the rest of the
+    // last word here
+    if ((hblk & 3) != 0 && lane == 0) hw[static_cast<int64_t>(hblk >> 2) * slots + r] = 0x7F7F7F7Fu;
   }
 }
 
@@ -220,11 +237,11 @@ cudaError_t launch_copy_kept_rows(int64_t rows, int cols, const void* src, const
 
 cudaError_t launch_gather_rows_q8(int64_t slots, int cols, const int* slot_token,
                                   const uint8_t* xq, const uint8_t* xs, const int* counts,
-                                  int64_t C, int64_t T, uint8_t* q, uint8_t* s, DevErr* err,
-                                  cudaStream_t st) {
+                                  int64_t C, int64_t T, uint8_t* q, uint32_t* xw, int hcols,
+                                  uint32_t* hw, DevErr* err, cudaStream_t st) {
   if (slots == 0) return cudaSuccess;
-  gather_rows_q8_kernel<<<row_blocks(slots), kThreads, 0, st>>>(slots, cols, slot_token, xq, xs,
-                                                                counts, C, T, q, s, err);
+  gather_rows_q8_kernel<<<row_blocks(slots), kThreads, 0, st>>>(
+      slots, cols, slot_token, xq, xs, counts, C, T, q, xw, hcols, hw, err);
   return cudaGetLastError();
 }
 

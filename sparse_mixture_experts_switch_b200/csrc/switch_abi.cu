@@ -1094,24 +1094,21 @@ switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
   a.N = cfg->n_experts;
   a.C = c.C;
   a.counts = counts;
-  a.xq = static_cast<const uint8_t*>(xq);
-  a.xs = static_cast<const uint8_t*>(x_scale);
-  if (!dispatched) {
-    // the slots' rows and, behind them, their scales (d_model / 128 bytes of
-    // a row's d_model that the 16-bit region has left)
-    uint8_t* q = c.at<uint8_t>(c.L.xdisp);
-    uint8_t* sc = q + S * cfg->d_model;
-    SMOE_TRY(launch_gather_rows_q8(S, cfg->d_model, slot_token, a.xq, a.xs, counts, c.C, cfg->T, q,
-                                   sc, c.err, c.st));
-    a.xq = q;
-    a.xs = sc;
-  }
   a.w1q = static_cast<const uint8_t*>(w1q);
   a.w1s = static_cast<const uint8_t*>(w1_scale);
   a.w2q = static_cast<const uint8_t*>(w2q);
   a.w2s = static_cast<const uint8_t*>(w2_scale);
+  // 8-bit rows and, behind them, their scale words, in the regions of the
+  // 16-bit rows: 4 ceil(cols / 512) bytes of a row's second cols bytes
+  uint8_t* q = c.at<uint8_t>(c.L.xdisp);
+  uint32_t* xw = reinterpret_cast<uint32_t*>(q + S * cfg->d_model);
   a.hq = c.at<uint8_t>(c.L.hbuf);
-  a.hs = a.hq + S * cfg->d_ff;
+  a.hw = reinterpret_cast<uint32_t*>(a.hq + S * cfg->d_ff);
+  SMOE_TRY(launch_gather_rows_q8(S, cfg->d_model, slot_token, static_cast<const uint8_t*>(xq),
+                                 static_cast<const uint8_t*>(x_scale), counts, c.C, cfg->T,
+                                 dispatched ? nullptr : q, xw, cfg->d_ff, a.hw, c.err, c.st));
+  a.xq = dispatched ? static_cast<const uint8_t*>(xq) : q;
+  a.xw = xw;
   a.y = y;
   a.err = c.err;
   a.spin = c.spin;
