@@ -154,11 +154,13 @@ cudaError_t launch_quantize_weights(int64_t n, int rows, int cols, const void* w
 
 // The experts' FFNs on 8-bit rows and weights (expert_ffn_q8.cu).
 struct FfnQ8Args {
-  int64_t A;                 // assignments (tokens x routes)
+  int64_t A, T;              // assignments (tokens x routes), tokens
   int d, F, N;
   int64_t C;
-  const uint8_t* xq;         // [N*C, d]
+  const uint8_t* xq;         // [N*C, d]; few: [T, d], or by slots with slot_token null
   const uint32_t* xw;        // scale words of its rows [ceil(d / 512)][N*C]
+  const uint8_t* xs;         // few: its scales [.., ceil(d / 128)]
+  const int* slot_token;     // few
   const int* counts;
   const uint8_t *w1q, *w1s, *w2q, *w2s;
   uint8_t* hq;               // [N*C, F] scratch
@@ -169,5 +171,9 @@ struct FfnQ8Args {
   int num_sms;
 };
 cudaError_t launch_expert_ffn_q8(const FfnQ8Args& a, cudaStream_t st);
+// The same for at most kFewTokens tokens an expert (expert_ffn_q8_few.cu): reads
+// the tokens' rows through slot_token itself; hw holds row-major scale bytes.
+constexpr int kFewTokens = 16;
+cudaError_t launch_expert_ffn_q8_few(const FfnQ8Args& a, cudaStream_t st);
 
 }  // namespace smoe

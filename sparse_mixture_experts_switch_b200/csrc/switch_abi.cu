@@ -1104,15 +1104,22 @@ switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
   uint32_t* xw = reinterpret_cast<uint32_t*>(q + S * cfg->d_model);
   a.hq = c.at<uint8_t>(c.L.hbuf);
   a.hw = reinterpret_cast<uint32_t*>(a.hq + S * cfg->d_ff);
-  SMOE_TRY(launch_gather_rows_q8(S, cfg->d_model, slot_token, static_cast<const uint8_t*>(xq),
-                                 static_cast<const uint8_t*>(x_scale), counts, c.C, cfg->T,
-                                 dispatched ? nullptr : q, xw, cfg->d_ff, a.hw, c.err, c.st));
-  a.xq = dispatched ? static_cast<const uint8_t*>(xq) : q;
-  a.xw = xw;
+  a.T = dispatched ? S : cfg->T;
   a.y = y;
   a.err = c.err;
   a.spin = c.spin;
   a.num_sms = c.num_sms;
+  a.xq = static_cast<const uint8_t*>(xq);
+  if (std::min(a.A, c.C) <= kFewTokens) {
+    a.xs = static_cast<const uint8_t*>(x_scale);
+    a.slot_token = dispatched ? nullptr : slot_token;
+    return cuda_status(launch_expert_ffn_q8_few(a, c.st));
+  }
+  SMOE_TRY(launch_gather_rows_q8(S, cfg->d_model, slot_token, a.xq,
+                                 static_cast<const uint8_t*>(x_scale), counts, c.C, cfg->T,
+                                 dispatched ? nullptr : q, xw, cfg->d_ff, a.hw, c.err, c.st));
+  if (!dispatched) a.xq = q;
+  a.xw = xw;
   return cuda_status(launch_expert_ffn_q8(a, c.st));
 }
 
