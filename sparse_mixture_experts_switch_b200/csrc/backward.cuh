@@ -7,8 +7,7 @@
 namespace smoe {
 
 enum BwdSched : int { kSchedRows = 0, kSchedWeight = 1, kSchedSplit = 2 };
-enum BwdEpi : int { kEpiDH = 0, kEpiStore = 1, kEpiDX = 2, kEpiStoreF32 = 3, kEpiDXSlot = 4,
-                    kEpiRows = 5 };
+enum BwdEpi : int { kEpiDH = 0, kEpiStore = 1, kEpiDX = 2, kEpiStoreF32 = 3, kEpiDXSlot = 4 };
 
 struct BwdParams {
   int N;                 // experts
@@ -28,7 +27,7 @@ struct BwdParams {
   const int* mtile_start;
   const int* slot_token;
   const __nv_bfloat16* h;      // dH epilogue: H [N*C, n_out]
-  __nv_bfloat16* out;          // dH: dA [N*C, n_out]; store: [N * M_out, n_out]; rows: [N*C, n_out]
+  __nv_bfloat16* out;          // dH: dA [N*C, n_out]; store: [N * M_out, n_out]
   float* out_f32;              // store-f32: [batches * M_out, n_out]; dX per slot: [N*C, n_out]
   float* dgp;                  // dH: [N*C, ntiles_n] partial gate gradients
   const __nv_bfloat16* dout;   // dX: [T, n_out]
@@ -81,10 +80,7 @@ cudaError_t launch_bwd_dw(const BwdFfnArgs& a, cudaStream_t st);
 // slots may hold one token) each kept slot's fp32 row dA W1_e + dh_s W_r is
 // stored at its slot instead, without the residual.
 cudaError_t launch_bwd_dx(const BwdFfnArgs& a, cudaStream_t st);
-// dx_disp [N*C, d] = dA W1_e, the kept slots' rows in bf16 (a.dx is that
-// buffer; no residual and no router term).
-cudaError_t launch_bwd_dx_rows(const BwdFfnArgs& a, cudaStream_t st);
-// launch_bwd_dx on operand-swapped CTA pairs (output features x slots per tile,
+// The same on operand-swapped CTA pairs (output features x slots per tile,
 // slots as the MMA's flexible N; backward_pair.cu).
 cudaError_t launch_bwd_dx_pair(const BwdFfnArgs& a, cudaStream_t st);
 // dW_r [N, d] = dh^T x on the tensor cores: dh as hi + lo bf16 planes

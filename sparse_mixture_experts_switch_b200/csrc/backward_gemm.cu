@@ -335,35 +335,6 @@ __device__ __forceinline__ void epi_dx_slot(const BwdParams& p, const BTile& t, 
   }
 }
 
-// dX rows of the staged FFN backward: kept slot rows in bf16.
-__device__ __forceinline__ void epi_rows(const BwdParams& p, const CUtensorMap* tmap_out,
-                                         const BTile& t, uint32_t taddr, int q, int lane,
-                                         uint32_t stg, int& nbox) {
-  const int64_t rbase = static_cast<int64_t>(t.m) * kBM + q * 32;
-  const int64_t cnt = p.counts[t.e];
-  const int64_t ne = cnt < p.C ? cnt : p.C;
-  const bool bulk = rbase + 32 <= ne;
-  const bool kept = rbase + lane < ne;
-  const int cols = p.n_out - t.n * kBN < kBN ? p.n_out - t.n * kBN : kBN;
-  const int64_t row0 = static_cast<int64_t>(t.e) * p.C + rbase;
-  for (int c = 0; c < cols / 32; ++c) {
-    uint32_t v[32], pk[16];
-    tmem_ld32_issue(taddr + static_cast<uint32_t>(c * 32), v);
-    tmem_ld_wait(v);
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      pk[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-    if (bulk) {
-      store_box(tmap_out, stg, nbox, pk, t.n * kBN + c * 32, static_cast<int>(row0), lane);
-    } else if (kept) {
-      uint4* dst = reinterpret_cast<uint4*>(p.out + (row0 + lane) * p.n_out + t.n * kBN + c * 32);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        dst[k] = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
-    }
-  }
-}
-
 }  // namespace
 
 template <int kSched, int kEpi>
@@ -551,8 +522,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) bwd_gemm_kernel(
     int nbox = 0;                      // running count: the two boxes alternate
     int acc = 0;
     uint32_t acc_phase = 0;
-    if (lane == 0 && (kEpi == kEpiDH || kEpi == kEpiStore || kEpi == kEpiRows))
-      tma_prefetch_desc(&tmap_a2);
+    if (lane == 0 && (kEpi == kEpiDH || kEpi == kEpiStore)) tma_prefetch_desc(&tmap_a2);
     prefetch_epilogue_rows<kEpi>(p, bwd_tile<kSched>(p, mts, blockIdx.x), q, lane);
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
       const bool ok = __all_sync(0xffffffffu, mbar_wait_sleepy(&tfull[acc], acc_phase, lim));
@@ -571,7 +541,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) bwd_gemm_kernel(
       if (kEpi == kEpiStore) epi_store<false>(p, &tmap_a2, t, taddr, q, lane, stg, nbox);
       else if (kEpi == kEpiStoreF32) epi_store<true>(p, &tmap_a2, t, taddr, q, lane, stg, nbox);
       else if (kEpi == kEpiDH) epi_dh(p, &tmap_a2, t, taddr, q, lane, stg, nbox);
-      else if (kEpi == kEpiRows) epi_rows(p, &tmap_a2, t, taddr, q, lane, stg, nbox);
       else if (kEpi == kEpiDXSlot) epi_dx_slot(p, t, taddr, q, lane);
       else epi_dx(p, t, taddr, q, lane);
       tc_fence_before();
@@ -951,22 +920,6 @@ cudaError_t launch_bwd_dx(const BwdFfnArgs& a, cudaStream_t st) {
     return run_bwd<kSchedRows, kEpiDXSlot>(ta, tb, ta2, tb2, p, a.num_sms, st);
   }
   return run_bwd<kSchedRows, kEpiDX>(ta, tb, ta2, tb2, p, a.num_sms, st);
-}
-
-cudaError_t launch_bwd_dx_rows(const BwdFfnArgs& a, cudaStream_t st) {
-  const uint64_t slots = static_cast<uint64_t>(a.N) * static_cast<uint64_t>(a.C);
-  CUtensorMap ta, tb, to;
-  bool ok = make_tmap_bf16_2d(&ta, a.da, a.F, slots, kBK, kBM);
-  ok = ok && make_tmap_bf16_2d(&tb, a.w1, a.d, static_cast<uint64_t>(a.N) * a.F, 64, 64);
-  ok = ok && make_tmap_bf16_2d(&to, a.dx, a.d, slots, 32, 32, true);
-  if (!ok) return cudaErrorInvalidValue;
-  BwdParams p = base_params(a);
-  p.K = a.F;
-  p.n_out = a.d;
-  p.ntiles_n = (a.d + kBN - 1) / kBN;
-  p.b_rows = a.F;
-  p.out = static_cast<__nv_bfloat16*>(a.dx);
-  return run_bwd<kSchedRows, kEpiRows>(ta, tb, to, tb, p, a.num_sms, st);
 }
 
 // Token chunks per term: about one wave of tiles over a B200's 148 SMs (a

@@ -39,15 +39,14 @@
 // eight MMAs.
 #include <cstring>
 
-#include "q8.cuh"
-#include "gemm_common.cuh"
+#include "pair_walk.cuh"
+#include "rows_gemm.cuh"
 
 namespace smoe {
 
 namespace {
 
 constexpr int kQK = 128;                               // K block: 128 codes
-constexpr int kQTok = 256;                             // most tokens of a tile
 constexpr int kQStages = 3;                            // of two K blocks
 constexpr uint32_t kQWBytes = 128 * kQK;               // 16 KB: 128 weight rows of a block
 constexpr uint32_t kQTokBytes = kQTok / 2 * kQK;       // 16 KB: up to 128 token rows
@@ -63,18 +62,15 @@ constexpr uint32_t kQStageOut = 128;                   // per drain warp: 32 tok
 constexpr uint32_t kQRedBytes = kQHalves * 2 * 4 * 128;   // maxima: [half][parity][quarter][32]
 constexpr uint32_t kQBarBytes = 512;
 constexpr uint32_t kQTmemCols = 512;
-// Limit of the last wait for copies in flight: a load takes microseconds.
-constexpr long long kDrainCycles = 40000000LL;
 constexpr uint32_t kQSmem = 1024 + kQStages * kQStageBytes + kQDrainWarps * kQStageOut +
                             kSfSlots * kSfBytes + kQRedBytes + kQBarBytes;   // + pts, kept
 
 struct Q8Params {
-  int N, n_out, K, ntiles_f;
-  int64_t C;
+  WalkParams walk;
+  int n_out, K;
   int kblk;                  // scale bytes of a weight row: ceil(K / 128)
   int nblk_w;                // weight blocks along n_out: ceil(n_out / 128)
   int64_t slots;             // N*C
-  const int* counts;
   const uint32_t* as;        // scale words of the rows [ceil(K / 512)][N*C]
   const uint8_t* ws;         // [N, nblk_w, kblk]
   uint8_t* hq;               // hidden: [N*C, n_out]
@@ -120,43 +116,6 @@ __host__ __device__ constexpr uint32_t idesc_q8(int M, int N) {
 }
 __device__ __forceinline__ uint32_t idesc_byte(uint32_t b) { return (b << 4) | (b << 29); }
 
-__device__ __forceinline__ int kept_q8(const Q8Params& p, int e) {
-  const int64_t c = p.counts[e];
-  return static_cast<int>(c < 0 ? 0 : (c < p.C ? c : p.C));
-}
-__device__ __forceinline__ int token_tiles(int kept) { return (kept + kQTok - 1) / kQTok; }
-
-// Per expert: its kept tokens, and the exclusive prefix of its tiles (token
-// tiles x feature tiles); one warp.
-__device__ void tiles_prefix_warp(const Q8Params& p, int* pts, int* kept) {
-  const int lane = threadIdx.x & 31;
-  const int per = (p.N + 31) / 32;
-  int s = 0;
-  for (int i = 0; i < per; ++i) {
-    const int e = lane * per + i;
-    if (e < p.N) {
-      const int k = kept_q8(p, e);
-      kept[e] = k;
-      s += token_tiles(k) * p.ntiles_f;
-    }
-  }
-  int inc = s;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, off);
-    if (lane >= off) inc += v;
-  }
-  int run = inc - s;
-  for (int i = 0; i < per; ++i) {
-    const int e = lane * per + i;
-    if (e < p.N) {
-      pts[e] = run;
-      run += token_tiles(kept[e]) * p.ntiles_f;
-    }
-  }
-  if (lane == 31) pts[p.N] = inc;
-}
-
 // First TMEM column of a tile's accumulator: even tiles grow from column 0, odd
 // ones end at the scales (column 448).  Two tiles in a row overlap where their
 // columns sum to more than 448, by 64 columns at most.
@@ -164,114 +123,12 @@ __device__ __forceinline__ uint32_t acc_column(int acc, int nmma) {
   return acc == 0 ? 0u : kSfTmem - static_cast<uint32_t>(nmma);
 }
 
-struct Q8TileAt {
-  int e;        // expert
-  int t0;       // first token slot of the tile within the expert
-  int nv;       // its tokens (1..256)
-  int nmma;     // the MMA's N: nv rounded up to 16
-  int f0;       // first output feature of the pair tile
-};
-
-__device__ __forceinline__ int small_div(int a, int b) {      // b is 1 or 2 most of the time
-  return b == 1 ? a : (b == 2 ? a >> 1 : a / b);
-}
-
-// Tiles in the order of a pair's walk (tile numbers that only grow).  An
-// expert's token tiles vary fastest, so pairs running side by side share the
-// weight tile.  The second product takes the list from its end: the last
-// experts' hidden rows, written last, are the ones still in L2.  The walk
-// remembers its expert: a search per tile would cost more than a short tile.
-template <bool kHidden>
-struct Q8Walk {
-  const Q8Params& p;
-  const int *pts, *kept;
-  int e;
-  __device__ __forceinline__ Q8Walk(const Q8Params& p_, const int* pts_, const int* kept_)
-      : p(p_), pts(pts_), kept(kept_), e(kHidden ? 0 : p_.N - 1) {}
-  __device__ __forceinline__ Q8TileAt at(int tile) {
-    if (!kHidden) tile = pts[p.N] - 1 - tile;
-    int steps = 0;
-    while (kHidden ? pts[e + 1] <= tile : pts[e] > tile) {
-      if (++steps > 8) {                     // far: halve the rest
-        int lo = kHidden ? e : 0, hi = kHidden ? p.N : e;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (pts[mid] <= tile) lo = mid; else hi = mid;
-        }
-        e = lo;
-        break;
-      }
-      e += kHidden ? 1 : -1;
-    }
-    Q8TileAt t;
-    t.e = e;
-    const int k = kept[e];
-    const int nt = token_tiles(k);
-    const int local = tile - pts[e];
-    const int mf = small_div(local, nt);
-    const int size = (small_div(k + nt - 1, nt) + 15) & ~15;
-    t.t0 = (local - mf * nt) * size;
-    t.nv = k - t.t0 < size ? k - t.t0 : size;
-    t.nmma = (t.nv + 15) & ~15;
-    t.f0 = mf * 256;
-    return t;
-  }
-};
-
-// Rows of the token boxes: the smallest of eight that holds half a tile (what a
-// box brings beyond it costs shared-memory bandwidth).
-constexpr int kQBoxes = 8;
-struct Q8Maps {
-  CUtensorMap w;
-  CUtensorMap tok[kQBoxes];
-};
-__host__ __device__ constexpr uint32_t box_rows(int box) {
-  return box < 3 ? 8u << box : (box == 3 ? 64u : 16u * box + 16u);   // 8 16 32 64 80 96 112 128
-}
-__device__ __forceinline__ int box_of(int half) {
-  return half <= 8 ? 0 : (half <= 16 ? 1 : (half <= 32 ? 2 : (half <= 64 ? 3 : (half - 1) >> 4)));
-}
-
 __device__ __forceinline__ void cp_async4_s(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-// relu of four fp32 values as e4m3 codes, `a` in the lowest byte.
-__device__ __forceinline__ uint32_t relu_e4m3x4(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-}
-
-// Lane j: an upper bound of the values v[j] of the warp's lanes (or 0 where all
-// are below it) with the scale of their maximum.  The bound has the upper 16
-// bits of the fp32 number, rounded up: a scale changes where the significand
-// passes 1.75, a border that 16 bits hold exactly, and numbers above zero order
-// as their bits.  Two tokens share a register; five exchanges halve the tokens
-// that a lane still follows (16 shuffles; a warp reduction per token, 32 of two
-// cycles of the whole SM each, took 310-940 cycles of a chunk's drain).
-__device__ __forceinline__ float warp_token_max(const uint32_t (&v)[32], int lane) {
-  uint32_t m[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    m[i] = __vmaxs2(__byte_perm(v[2 * i] + 0xFFFFu, v[2 * i + 1] + 0xFFFFu, 0x7632), 0u);
-#pragma unroll
-  for (int n = 8; n >= 1; n >>= 1) {                 // lane bit 2 n picks the upper half
-    const bool up = (lane & (2 * n)) != 0;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const uint32_t keep = up ? m[i + n] : m[i];
-      const uint32_t send = up ? m[i] : m[i + n];
-      m[i] = __vmaxs2(keep, __shfl_xor_sync(0xffffffffu, send, 2 * n));
-    }
-  }
-  const uint32_t p = __vmaxs2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
-  return __uint_as_float((lane & 1) ? p & 0xFFFF0000u : p << 16);
-}
-
 template <bool kHidden>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
-    expert_gemm_q8_kernel(const __grid_constant__ Q8Maps maps, Q8Params p) {
+    expert_gemm_q8_kernel(const __grid_constant__ RowMaps maps, Q8Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -289,7 +146,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* pts = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + kQBarBytes);   // [N + 1]
-  int* kept = pts + p.N + 1;                                                          // [N]
+  int* kept = pts + p.walk.N + 1;                                                          // [N]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -299,7 +156,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
   const long long lim = p.spin;
   const int kblocks = (p.K + kQK - 1) / kQK;
 
-  if (warp == 0) tiles_prefix_warp(p, pts, kept);
+  if (warp == 0) tiles_prefix_warp(p.walk, pts, kept);
   if (threadIdx.x == 32) {
     for (int s = 0; s < kQStages; ++s) {
       mbar_init(&full[s], 2);               // the leader's two loading warps
@@ -321,7 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
     fence_barrier_init();
   }
   __syncthreads();
-  const int total = pts[p.N];
+  const int total = pts[p.walk.N];
   if (cid >= total) return;                 // same decision in both CTAs of the pair
   if (warp == 1) {
     tmem_alloc_pair(tmem_holder, kQTmemCols);
@@ -337,22 +194,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
   const uint32_t tempty_lead = map_to_rank(smem_u32(tempty), 0);
   const uint32_t tover_lead = map_to_rank(smem_u32(tover), 0);
 
-  Q8Walk<kHidden> walk(p, pts, kept);
+  RowWalk<kHidden> walk(p.walk, pts, kept);
   const int kstages = (kblocks + 1) / 2;
   if (warp == 0 || warp == 2) {
     // ------------------------------ TMA: warp 0 the weights, warp 2 the tokens
     const bool tokens = warp == 2;
-    if (elect_one()) tma_prefetch_desc(tokens ? &maps.tok[kQBoxes - 1] : &maps.w);
+    if (elect_one()) tma_prefetch_desc(tokens ? &maps.tok[kRowBoxes - 1] : &maps.w);
     int stage = 0;
     uint32_t phase = 0;
     uint32_t issued_mask = 0, issued_phase = 0;
     for (int tile = cid; tile < total; tile += ncl) {
       if (__any_sync(0xffffffffu, *abort_flag)) break;
-      const Q8TileAt t = walk.at(tile);
+      const RowTile t = walk.at(tile);
       const int half = t.nmma >> 1;
       const int box = box_of(half);
       const CUtensorMap* map = tokens ? &maps.tok[box] : &maps.w;
-      const int row = tokens ? static_cast<int>(static_cast<int64_t>(t.e) * p.C + t.t0 +
+      const int row = tokens ? static_cast<int>(static_cast<int64_t>(t.e) * p.walk.C + t.t0 +
                                                 static_cast<int>(rank) * half)
                              : t.f0 + static_cast<int>(rank) * 128;
       const uint32_t bytes = tokens ? box_rows(box) * kQK : kQWBytes;
@@ -393,7 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
     if (leader && lane == 0) {
       for (int s = 0; s < kQStages; ++s)
         if (((issued_mask >> s) & 1u) &&
-            !mbar_wait_cluster(&full[s], (issued_phase >> s) & 1u, kDrainCycles))
+            !mbar_wait_cluster(&full[s], (issued_phase >> s) & 1u, kCopyDrainCycles))
           report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereDrain, s);
     }
   } else if (warp == 3) {
@@ -406,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
     const int groups = (kblocks + 3) / 4;
     const bool words = (p.kblk & 3) == 0;
     int tile = cid, g = 0;
-    Q8TileAt t{};
+    RowTile t{};
     const uint8_t* wrow = nullptr;
     auto enter = [&]() {
       t = walk.at(tile);
@@ -428,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
       }
       const uint32_t dst = smem_u32(sf + slot * kSfBytes) + lane * 16;
       const uint32_t* src =
-          p.as + static_cast<int64_t>(g) * p.slots + static_cast<int64_t>(t.e) * p.C + t.t0;
+          p.as + static_cast<int64_t>(g) * p.slots + static_cast<int64_t>(t.e) * p.walk.C + t.t0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {                    // rows past the last: any scale
         const int r = 32 * j + lane;
@@ -585,25 +442,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
       }
     };
     for (int tile = cid; tile < total; tile += ncl) {
-      const bool ok = __all_sync(0xffffffffu, mbar_wait_sleepy(&tfull[acc], acc_phase, lim));
-      // The four warps of a half meet at a barrier for each hidden chunk: they
-      // go on, or leave, together.
-      if (kHidden) {
-        int all_ok;
-        asm volatile(
-            "{\n .reg .pred p, r;\n setp.ne.b32 p, %1, 0;\n"
-            " barrier.cta.red.and.pred r, %2, 128, p;\n selp.u32 %0, 1, 0, r;\n}\n"
-            : "=r"(all_ok)
-            : "r"(ok ? 1 : 0), "r"(1 + h)
-            : "memory");
-        if (!all_ok) {
-          if (lane == 0) {
-            report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmEpilogue, tile);
-            *abort_flag = 1;
-          }
-          break;
-        }
-      } else if (!ok) {
+      bool ok = __all_sync(0xffffffffu, mbar_wait_sleepy(&tfull[acc], acc_phase, lim));
+      if (kHidden) ok = all_of_barrier(ok, 1 + h);   // they meet below: go on together
+      if (!ok) {
         if (lane == 0) {
           report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmEpilogue, tile);
           *abort_flag = 1;
@@ -611,12 +452,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         break;
       }
       tc_fence_after();
-      const Q8TileAt t = walk.at(tile);
+      const RowTile t = walk.at(tile);
       const int fc = t.f0 + static_cast<int>(rank) * 128;          // the CTA's first feature
       const int fb = fc + q * 32;                                  // the warp's
       const bool on = fb < p.n_out;                                // warp-uniform
       const int nch = (t.nv + 31) >> 5;
-      const int64_t row0 = static_cast<int64_t>(t.e) * p.C + t.t0;
+      const int64_t row0 = static_cast<int64_t>(t.e) * p.walk.C + t.t0;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                              acc_column(acc, t.nmma);
       if (h >= 2 || h >= nch) arrive_lead(tover, tover_lead, acc);   // none of those
@@ -632,7 +473,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         const int j0 = c * 32;
         const int jn = t.nv - j0 < 32 ? t.nv - j0 : 32;            // tokens of the chunk
         if (kHidden) {
-          const float mine = warp_token_max(v, lane);
+          // the maximum as an upper bound with the same scale: the upper 16 bits of
+          // the fp32 number, rounded up (a scale changes where the significand passes
+          // 1.75, a border that 16 bits hold; numbers above zero order as their bits,
+          // those below become 0, the ReLU)
+          uint32_t m[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            m[i] = __vmaxs2(__byte_perm(v[2 * i] + 0xFFFFu, v[2 * i + 1] + 0xFFFFu, 0x7632), 0u);
+          const float mine = __uint_as_float(warp_token_max(m, lane));
           float* r = redh + par * 128;
           par ^= 1;
           r[q * 32 + lane] = mine;
@@ -655,10 +504,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
             const uint32_t w = relu_e4m3x4(
                 __uint_as_float(v[4 * k]) * sc[k].x, __uint_as_float(v[4 * k + 1]) * sc[k].y,
                 __uint_as_float(v[4 * k + 2]) * sc[k].z, __uint_as_float(v[4 * k + 3]) * sc[k].w);
-            const uint32_t t1 = __shfl_xor_sync(0xffffffffu, w, 1);
-            const uint32_t x = (lane & 1) ? __byte_perm(t1, w, 0x7351) : __byte_perm(w, t1, 0x6240);
-            const uint32_t t2 = __shfl_xor_sync(0xffffffffu, x, 2);
-            const uint32_t z = (lane & 2) ? __byte_perm(t2, x, 0x7632) : __byte_perm(x, t2, 0x5410);
+            const uint32_t z = transpose_bytes(w, lane);
             const int rr = 4 * k + (lane & 3);
             if (rr < jn)
               *reinterpret_cast<uint32_t*>(p.hq + (row0 + j0 + rr) * p.n_out + fb + (lane & ~3)) = z;
@@ -674,8 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
             const uint32_t w = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-            const uint32_t o = __shfl_xor_sync(0xffffffffu, w, 1);
-            const uint32_t z = (lane & 1) ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+            const uint32_t z = transpose_halves(w, lane);
             if (j + (lane & 1) < jn)
               *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * p.n_out) = z;
           }
@@ -725,13 +570,13 @@ bool map_weights(CUtensorMap* m, const void* base, int N, int n_out, int K) {
 template <bool kHidden>
 cudaError_t run_q8(const void* rows, const void* weights, const Q8Params& p, int num_sms,
                    cudaStream_t st) {
-  const int64_t slots = static_cast<int64_t>(p.N) * p.C;
-  Q8Maps maps;
-  bool ok = map_weights(&maps.w, weights, p.N, p.n_out, p.K);
-  for (int i = 0; i < kQBoxes; ++i)
+  const int64_t slots = static_cast<int64_t>(p.walk.N) * p.walk.C;
+  RowMaps maps;
+  bool ok = map_weights(&maps.w, weights, p.walk.N, p.n_out, p.K);
+  for (int i = 0; i < kRowBoxes; ++i)
     ok = ok && map_rows(&maps.tok[i], rows, slots, p.K, box_rows(i));
   if (!ok) return cudaErrorInvalidValue;
-  const size_t smem = kQSmem + sizeof(int) * (2 * p.N + 1);
+  const size_t smem = kQSmem + sizeof(int) * (2 * p.walk.N + 1);
   static size_t smem_set[64] = {};
   cudaError_t e = ensure_smem_limit(
       reinterpret_cast<const void*>(&expert_gemm_q8_kernel<kHidden>), smem, smem_set);
@@ -746,14 +591,14 @@ cudaError_t run_q8(const void* rows, const void* weights, const Q8Params& p, int
 cudaError_t launch_expert_ffn_q8(const FfnQ8Args& a, cudaStream_t st) {
   const int64_t slots = static_cast<int64_t>(a.N) * a.C;
   Q8Params p{};
-  p.N = a.N;
+  p.walk.N = a.N;
   p.n_out = a.F;
   p.K = a.d;
-  p.ntiles_f = (a.F + 255) / 256;
-  p.C = a.C;
+  p.walk.ntiles_f = (a.F + 255) / 256;
+  p.walk.C = a.C;
   p.kblk = static_cast<int>(q8_blocks(a.d));
   p.nblk_w = static_cast<int>(q8_blocks(a.F));
-  p.counts = a.counts;
+  p.walk.counts = a.counts;
   p.slots = slots;
   p.as = a.xw;
   p.ws = a.w1s;
@@ -765,7 +610,7 @@ cudaError_t launch_expert_ffn_q8(const FfnQ8Args& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   p.n_out = a.d;
   p.K = a.F;
-  p.ntiles_f = (a.d + 255) / 256;
+  p.walk.ntiles_f = (a.d + 255) / 256;
   p.kblk = static_cast<int>(q8_blocks(a.F));
   p.nblk_w = static_cast<int>(q8_blocks(a.d));
   p.as = a.hw;

@@ -1,0 +1,181 @@
+// Walk of CTA pairs over tiles of "output features x one expert's tokens", with
+// the tokens as the MMA's flexible N, and the pieces that the drains of such
+// tiles share (one feature a lane, 32 tokens a chunk).
+#pragma once
+
+#include "q8.cuh"
+
+namespace smoe {
+
+constexpr int kQTok = 256;                             // most tokens of a tile
+
+struct WalkParams {
+  int N;                     // experts
+  int ntiles_f;              // 256-feature tiles of an expert
+  int64_t C;
+  const int* counts;
+};
+
+__device__ __forceinline__ int kept_tokens(const WalkParams& p, int e) {
+  const int64_t c = p.counts[e];
+  return static_cast<int>(c < 0 ? 0 : (c < p.C ? c : p.C));
+}
+__device__ __forceinline__ int token_tiles(int kept) { return (kept + kQTok - 1) / kQTok; }
+
+// Per expert: its kept tokens, and the exclusive prefix of its tiles (token
+// tiles x feature tiles); one warp.
+static __device__ void tiles_prefix_warp(const WalkParams& p, int* pts, int* kept) {
+  const int lane = threadIdx.x & 31;
+  const int per = (p.N + 31) / 32;
+  int s = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    if (e < p.N) {
+      const int k = kept_tokens(p, e);
+      kept[e] = k;
+      s += token_tiles(k) * p.ntiles_f;
+    }
+  }
+  int inc = s;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += v;
+  }
+  int run = inc - s;
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    if (e < p.N) {
+      pts[e] = run;
+      run += token_tiles(kept[e]) * p.ntiles_f;
+    }
+  }
+  if (lane == 31) pts[p.N] = inc;
+}
+
+struct RowTile {
+  int e;        // expert
+  int t0;       // first token slot of the tile within the expert
+  int nv;       // its tokens (1..256)
+  int nmma;     // the MMA's N: nv rounded up to 16
+  int f0;       // first output feature of the pair tile
+};
+
+__device__ __forceinline__ int small_div(int a, int b) {      // b is 1 or 2 most of the time
+  return b == 1 ? a : (b == 2 ? a >> 1 : a / b);
+}
+
+// Tiles in the order of a pair's walk (tile numbers that only grow).  An
+// expert's token tiles vary fastest, so pairs running side by side share the
+// weight tile.  A product that reads what the one before it wrote takes the list
+// from its end (kForward false): the last experts' rows, written last, are the
+// ones still in L2.  The walk
+// remembers its expert: a search per tile would cost more than a short tile.
+template <bool kForward>
+struct RowWalk {
+  const WalkParams& p;
+  const int *pts, *kept;
+  int e;
+  __device__ __forceinline__ RowWalk(const WalkParams& p_, const int* pts_, const int* kept_)
+      : p(p_), pts(pts_), kept(kept_), e(kForward ? 0 : p_.N - 1) {}
+  __device__ __forceinline__ RowTile at(int tile) {
+    if (!kForward) tile = pts[p.N] - 1 - tile;
+    int steps = 0;
+    while (kForward ? pts[e + 1] <= tile : pts[e] > tile) {
+      if (++steps > 8) {                     // far: halve the rest
+        int lo = kForward ? e : 0, hi = kForward ? p.N : e;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (pts[mid] <= tile) lo = mid; else hi = mid;
+        }
+        e = lo;
+        break;
+      }
+      e += kForward ? 1 : -1;
+    }
+    RowTile t;
+    t.e = e;
+    const int k = kept[e];
+    const int nt = token_tiles(k);
+    const int local = tile - pts[e];
+    const int mf = small_div(local, nt);
+    const int size = (small_div(k + nt - 1, nt) + 15) & ~15;
+    t.t0 = (local - mf * nt) * size;
+    t.nv = k - t.t0 < size ? k - t.t0 : size;
+    t.nmma = (t.nv + 15) & ~15;
+    t.f0 = mf * 256;
+    return t;
+  }
+};
+
+// Rows of the token boxes: the smallest of eight that holds half a tile (what a
+// box brings beyond it costs shared-memory bandwidth).
+constexpr int kRowBoxes = 8;
+struct RowMaps {
+  CUtensorMap w;
+  CUtensorMap tok[kRowBoxes];
+};
+__host__ __device__ constexpr uint32_t box_rows(int box) {
+  return box < 3 ? 8u << box : (box == 3 ? 64u : 16u * box + 16u);   // 8 16 32 64 80 96 112 128
+}
+__device__ __forceinline__ int box_of(int half) {
+  return half <= 8 ? 0 : (half <= 16 ? 1 : (half <= 32 ? 2 : (half <= 64 ? 3 : (half - 1) >> 4)));
+}
+
+// relu of four fp32 values as e4m3 codes, `a` in the lowest byte.
+__device__ __forceinline__ uint32_t relu_e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// Lane j: the maximum over the warp of token j, from 16 registers of two tokens
+// each (token 2 i in the low half of m[i]) compared as signed 16-bit numbers; the
+// result in the upper half.  Five exchanges halve the tokens that a lane still
+// follows: 16 shuffles (a warp reduction per token, 32 of two cycles of the whole
+// SM each, took 310-940 cycles of a chunk's drain).
+__device__ __forceinline__ uint32_t warp_token_max(uint32_t (&m)[16], int lane) {
+#pragma unroll
+  for (int n = 8; n >= 1; n >>= 1) {                 // lane bit 2 n picks the upper half
+    const bool up = (lane & (2 * n)) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const uint32_t keep = up ? m[i + n] : m[i];
+      const uint32_t send = up ? m[i] : m[i + n];
+      m[i] = __vmaxs2(keep, __shfl_xor_sync(0xffffffffu, send, 2 * n));
+    }
+  }
+  const uint32_t p = __vmaxs2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+  return (lane & 1) ? p & 0xFFFF0000u : p << 16;
+}
+
+// Words w of tokens 4k .. 4k + 3 (one byte each, a feature a lane) as four
+// features of token 4k + lane % 4: the transpose of four lanes' words.
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int lane) {
+  const uint32_t t1 = __shfl_xor_sync(0xffffffffu, w, 1);
+  const uint32_t x = (lane & 1) ? __byte_perm(t1, w, 0x7351) : __byte_perm(w, t1, 0x6240);
+  const uint32_t t2 = __shfl_xor_sync(0xffffffffu, x, 2);
+  return (lane & 2) ? __byte_perm(t2, x, 0x7632) : __byte_perm(x, t2, 0x5410);
+}
+// Tokens j and j + 1 of this feature (16 bits each) as two features of token
+// j + lane % 2.
+__device__ __forceinline__ uint32_t transpose_halves(uint32_t w, int lane) {
+  const uint32_t o = __shfl_xor_sync(0xffffffffu, w, 1);
+  return (lane & 1) ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+}
+// Bits of token `lane` over the warp's features as this feature's bits over the
+// 32 tokens.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
+  const uint32_t masks[5] = {0x0000FFFFu, 0x00FF00FFu, 0x0F0F0F0Fu, 0x33333333u, 0x55555555u};
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const int s = 16 >> i;
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, s);
+    x = (lane & s) ? (x & ~masks[i]) | ((y & ~masks[i]) >> s)
+                   : (x & masks[i]) | ((y & masks[i]) << s);
+  }
+  return x;
+}
+
+}  // namespace smoe

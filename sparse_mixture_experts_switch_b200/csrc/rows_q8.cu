@@ -76,9 +76,21 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(
   }
 }
 
+// 0x80 in each byte that holds a code above zero.
+__device__ __forceinline__ uint32_t positive_codes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & ~w & 0x80808080u;
+}
+// The four flags as bits 0 .. 3.
+__device__ __forceinline__ uint32_t flag_bits(uint32_t f) {
+  return ((f >> 7) * 0x01020408u) >> 24;
+}
+
+// Zero rows up to the next multiple of 64 (kPad), or the kept rows' bits.
+template <bool kPad, bool kMask>
 __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(
     int64_t rows, int cols, const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
-    const int* __restrict__ counts, int64_t C, uint4* __restrict__ out) {
+    const int* __restrict__ counts, int64_t C, uint4* __restrict__ out,
+    uint8_t* __restrict__ mask) {
   const int lane = threadIdx.x & 31;
   const int nv = cols / 8;
   const int64_t nblk = q8_blocks(cols);
@@ -88,28 +100,18 @@ __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(
     const int64_t e = r / C, i = r - e * C;
     const int64_t kept = kept_of(counts, C, e);
     if (i >= kept) {
-      if (i < (kept + 63) / 64 * 64)
+      if (kPad && i < (kept + 63) / 64 * 64)
         for (int v = lane; v < nv; v += 32) out[r * nv + v] = make_uint4(0, 0, 0, 0);
       continue;
     }
     const uint2* row = reinterpret_cast<const uint2*>(q + r * cols);
-    for (int v = lane; v < nv; v += 32)
-      out[r * nv + v] = q8_decode8(__ldg(row + v), __ldg(s + r * nblk + v / 16));
-  }
-}
-
-__global__ void __launch_bounds__(kThreads) copy_kept_rows_kernel(
-    int64_t rows, int nv, const uint4* __restrict__ src, const int* __restrict__ counts, int64_t C,
-    uint4* __restrict__ dst) {
-  const int lane = threadIdx.x & 31;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < rows;
-       r += step) {
-    const int64_t e = r / C, i = r - e * C;
-    const int64_t kept = kept_of(counts, C, e);
-    if (i >= (kept + 63) / 64 * 64) continue;
-    for (int v = lane; v < nv; v += 32)
-      dst[r * nv + v] = i < kept ? __ldg(src + r * nv + v) : make_uint4(0, 0, 0, 0);
+    for (int v = lane; v < nv; v += 32) {
+      const uint2 w = __ldg(row + v);
+      out[r * nv + v] = q8_decode8(w, __ldg(s + r * nblk + v / 16));
+      if (kMask)
+        mask[r * nv + v] = static_cast<uint8_t>(flag_bits(positive_codes(w.x)) |
+                                                flag_bits(positive_codes(w.y)) << 4);
+    }
   }
 }
 
@@ -220,18 +222,18 @@ cudaError_t launch_quantize_rows(int64_t rows, int cols, const void* src, const 
 }
 
 cudaError_t launch_unpack_rows(int64_t rows, int cols, const uint8_t* q, const uint8_t* s,
-                               const int* counts, int64_t C, void* out, cudaStream_t st) {
+                               const int* counts, int64_t C, void* out, uint32_t* mask, bool pad,
+                               cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  unpack_rows_kernel<<<row_blocks(rows), kThreads, 0, st>>>(rows, cols, q, s, counts, C,
-                                                            static_cast<uint4*>(out));
-  return cudaGetLastError();
-}
-
-cudaError_t launch_copy_kept_rows(int64_t rows, int cols, const void* src, const int* counts,
-                                  int64_t C, void* dst, cudaStream_t st) {
-  if (rows == 0) return cudaSuccess;
-  copy_kept_rows_kernel<<<row_blocks(rows), kThreads, 0, st>>>(
-      rows, cols / 8, static_cast<const uint4*>(src), counts, C, static_cast<uint4*>(dst));
+  auto* o = static_cast<uint4*>(out);
+  auto* m = reinterpret_cast<uint8_t*>(mask);
+  const int g = row_blocks(rows);
+  if (pad)
+    unpack_rows_kernel<true, false><<<g, kThreads, 0, st>>>(rows, cols, q, s, counts, C, o, nullptr);
+  else if (mask != nullptr)
+    unpack_rows_kernel<false, true><<<g, kThreads, 0, st>>>(rows, cols, q, s, counts, C, o, m);
+  else
+    unpack_rows_kernel<false, false><<<g, kThreads, 0, st>>>(rows, cols, q, s, counts, C, o, nullptr);
   return cudaGetLastError();
 }
 

@@ -7,7 +7,7 @@
 #include <cstring>
 
 #include "backward.cuh"
-#include "q8.cuh"
+#include "rows_gemm.cuh"
 
 using namespace smoe;
 
@@ -48,7 +48,7 @@ struct Layout {
   // sums of dh, dropped-token list and its counter; top-2 and fp32 only:
   // the dX GEMM's fp32 rows per slot
   size_t probs_s, da, dgp, dh, dhp, dhs, wrp, dgate, rpart, colsum, drop_list, n_drop, dxs,
-      bwd_total;
+      mask, bwd_total;
 };
 
 // Bytes 16..19 of the workspace: the loss kernel's completion ticket (kept
@@ -118,6 +118,8 @@ Layout layout_for(const switch_config_t& c, int64_t C) {
   L.dxs = take(routes_of(c) == 2 || c.dtype != SWITCH_BF16
                    ? sizeof(float) * slots * static_cast<size_t>(c.d_model)
                    : 0);
+  // a bit per hidden value (the backward from 8-bit checkpoints)
+  L.mask = take(c.dtype == SWITCH_BF16 ? slots * static_cast<size_t>(c.d_ff) / 8 : 0);
   L.bwd_total = o;
   return L;
 }
@@ -1123,6 +1125,18 @@ switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
   return cuda_status(launch_expert_ffn_q8(a, c.st));
 }
 
+// What the products over experts' rows have in common.
+static RowsGemmArgs rows_args(const switch_config_t* cfg, const Ctx& c, const int32_t* counts) {
+  RowsGemmArgs a{};
+  a.N = cfg->n_experts;
+  a.C = c.C;
+  a.counts = counts;
+  a.err = c.err;
+  a.spin = c.spin;
+  a.num_sms = c.num_sms;
+  return a;
+}
+
 switch_status_t switch_expert_ffn_checkpoint(const switch_config_t* cfg, const void* x,
                                              const int32_t* slot_token, const int32_t* counts,
                                              const void* w1, const void* w2, void* y, void* xq,
@@ -1139,38 +1153,26 @@ switch_status_t switch_expert_ffn_checkpoint(const switch_config_t* cfg, const v
   s = prepare(cfg, ws, ws_bytes, stream, &c);
   if (s != SWITCH_OK) return s;
   const int64_t S = static_cast<int64_t>(cfg->n_experts) * c.C;
-  FfnArgs a{};
-  a.T = cfg->T;
-  a.d = cfg->d_model;
-  a.F = cfg->d_ff;
-  a.N = cfg->n_experts;
-  a.C = c.C;
-  a.slot_token = slot_token;
-  a.counts = counts;
-  a.mtile_start = c.at<int>(c.L.mtile_start);
-  a.w1 = w1;
-  a.w2 = w2;
-  a.hbuf = c.ws + c.L.hbuf;
-  a.y = y;
-  a.mode2 = kModeY;
-  a.err = c.err;
-  a.spin = c.spin;
-  a.num_sms = c.num_sms;
-  a.pair1 = (cfg->flags & SWITCH_FLAG_GEMM_PAIRS) != 0;
-  a.pair2 = !(cfg->flags & SWITCH_FLAG_GEMM_1SM);
-  switch_config_t by_copy = *cfg;            // the rows are always copied here
-  by_copy.flags &= ~SWITCH_FLAG_GATHER_IN_GEMM;
-  a.pair1_rows = gemm1_rows_pairs(&by_copy, c.C);
-  a.x_disp = dispatched ? x : c.ws + c.L.xdisp;
-  SMOE_TRY(launch_mtile_table(a.N, a.C, counts, c.at<int>(c.L.mtile_start), c.st));
-  SMOE_TRY(launch_quantize_rows(S, a.d, x, counts, c.C, dispatched ? nullptr : slot_token, cfg->T,
-                                dispatched ? nullptr : c.ws + c.L.xdisp, false,
+  const void* rows = dispatched ? x : c.ws + c.L.xdisp;
+  SMOE_TRY(launch_quantize_rows(S, cfg->d_model, x, counts, c.C, dispatched ? nullptr : slot_token,
+                                cfg->T, dispatched ? nullptr : c.ws + c.L.xdisp, false,
                                 static_cast<uint8_t*>(xq), static_cast<uint8_t*>(x_scale), c.err,
                                 c.st));
-  SMOE_TRY(launch_expert_ffn_bf16(a, c.st));
-  return cuda_status(launch_quantize_rows(S, a.F, a.hbuf, counts, c.C, nullptr, 0, nullptr, true,
-                                          static_cast<uint8_t*>(hq),
-                                          static_cast<uint8_t*>(h_scale), c.err, c.st));
+  RowsGemmArgs a = rows_args(cfg, c, counts);
+  a.n_out = cfg->d_ff;
+  a.K = cfg->d_model;
+  a.rows = rows;
+  a.w = w1;
+  a.out = c.ws + c.L.hbuf;
+  a.hq = static_cast<uint8_t*>(hq);
+  a.hs = static_cast<uint8_t*>(h_scale);
+  SMOE_TRY(launch_rows_hidden(a, c.st));
+  a.n_out = cfg->d_model;
+  a.K = cfg->d_ff;
+  a.rows = c.ws + c.L.hbuf;
+  a.w = w2;
+  a.out = y;
+  return cuda_status(launch_rows_out(a, c.st));
 }
 
 switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const void* xq,
@@ -1193,39 +1195,51 @@ switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const 
   s = prepare(cfg, ws, ws_bytes, stream, &c);
   if (s != SWITCH_OK) return s;
   const int64_t S = static_cast<int64_t>(cfg->n_experts) * c.C;
-  BwdFfnArgs b{};
-  b.T = cfg->T;
-  b.d = cfg->d_model;
-  b.F = cfg->d_ff;
-  b.N = cfg->n_experts;
-  b.C = c.C;
-  b.counts = counts;
-  b.mtile_start = c.at<int>(c.L.mtile_start);
-  b.w1 = w1;
-  b.w2 = w2;
-  b.x_disp = c.ws + c.L.xdisp;
-  b.hbuf = c.ws + c.L.hbuf;
-  b.dys = c.ws + c.L.ybuf;
-  b.da = c.ws + c.L.da;
-  b.dgp = c.at<float>(c.L.dgp);
-  b.dw1 = dw1;
-  b.dw2 = dw2;
-  b.dx = dx;
-  b.pair_dw = !(cfg->flags & SWITCH_FLAG_GEMM_1SM);
-  b.err = c.err;
-  b.spin = c.spin;
-  b.num_sms = c.num_sms;
-  SMOE_TRY(launch_mtile_table(b.N, b.C, counts, c.at<int>(c.L.mtile_start), c.st));
-  SMOE_TRY(launch_unpack_rows(S, b.d, static_cast<const uint8_t*>(xq),
-                              static_cast<const uint8_t*>(x_scale), counts, c.C,
-                              c.ws + c.L.xdisp, c.st));
-  SMOE_TRY(launch_unpack_rows(S, b.F, static_cast<const uint8_t*>(hq),
-                              static_cast<const uint8_t*>(h_scale), counts, c.C,
-                              c.ws + c.L.hbuf, c.st));
-  SMOE_TRY(launch_copy_kept_rows(S, b.d, dy, counts, c.C, c.ws + c.L.ybuf, c.st));
-  SMOE_TRY(launch_bwd_dh(b, c.st));
-  SMOE_TRY(launch_bwd_dw(b, c.st));
-  return cuda_status(launch_bwd_dx_rows(b, c.st));
+  const int d = cfg->d_model, F = cfg->d_ff;
+  uint8_t* xb = c.ws + c.L.xdisp;
+  uint8_t* hb = c.ws + c.L.hbuf;
+  uint32_t* mask = c.at<uint32_t>(c.L.mask);
+  SMOE_TRY(launch_unpack_rows(S, F, static_cast<const uint8_t*>(hq),
+                              static_cast<const uint8_t*>(h_scale), counts, c.C, hb, mask, false,
+                              c.st));
+  // dw2 = dy^T h while h is fresh, da = (dy w2) where h > 0, dx = da w1,
+  // dw1 = da^T x
+  WeightGradArgs g{};
+  g.N = cfg->n_experts;
+  g.C = c.C;
+  g.counts = counts;
+  g.err = c.err;
+  g.spin = c.spin;
+  g.num_sms = c.num_sms;
+  g.M = d;
+  g.Nn = F;
+  g.a = dy;
+  g.b = hb;
+  g.dw = dw2;
+  SMOE_TRY(launch_weight_grad(g, c.st));
+  RowsGemmArgs a = rows_args(cfg, c, counts);
+  a.n_out = F;
+  a.K = d;
+  a.rows = dy;
+  a.w = w2;
+  a.out = c.ws + c.L.da;
+  a.mask = mask;
+  SMOE_TRY(launch_rows_da(a, c.st));
+  a.n_out = d;
+  a.K = F;
+  a.rows = c.ws + c.L.da;
+  a.w = w1;
+  a.out = dx;
+  SMOE_TRY(launch_rows_dx(a, c.st));
+  SMOE_TRY(launch_unpack_rows(S, d, static_cast<const uint8_t*>(xq),
+                              static_cast<const uint8_t*>(x_scale), counts, c.C, xb, nullptr,
+                              false, c.st));
+  g.M = F;
+  g.Nn = d;
+  g.a = c.ws + c.L.da;
+  g.b = xb;
+  g.dw = dw1;
+  return cuda_status(launch_weight_grad(g, c.st));
 }
 
 // What switch_layer_forward (SWITCH_FLAG_TRAINING) keeps, outside the
@@ -1306,7 +1320,8 @@ switch_status_t switch_checkpoint_load(const switch_config_t* cfg, const void* x
   SMOE_TRY(launch_gather_rows(S, static_cast<int64_t>(cfg->d_model) * 2,
                               c.at<int>(c.L.slot_token), x, c.ws + c.L.xdisp, c.st));
   return cuda_status(launch_unpack_rows(S, cfg->d_ff, in + k.hq, in + k.hs,
-                                        c.at<int>(c.L.counts), c.C, c.ws + c.L.hbuf, c.st));
+                                        c.at<int>(c.L.counts), c.C, c.ws + c.L.hbuf, nullptr,
+                                        true, c.st));
 }
 
 switch_status_t switch_get_device_error(void* ws, void* stream, int32_t* where_out,
