@@ -120,7 +120,7 @@ struct NormBwdArgs {
   float* part;               // [kNormParts][d] scratch
   int num_sms;
 };
-constexpr int kNormParts = 592;        // rows of partial gain gradients (4 per SM of a B200)
+constexpr int kNormParts = 296;        // rows of partial gain gradients (2 per SM of a B200)
 cudaError_t launch_residual_norm_backward(const NormBwdArgs& a, cudaStream_t st);
 
 // Quantises rows [rows, cols] bf16 (rows_q8.cu).  counts: rows are the slots
