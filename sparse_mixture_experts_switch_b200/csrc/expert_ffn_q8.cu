@@ -157,6 +157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
   const int kblocks = (p.K + kQK - 1) / kQK;
 
   if (warp == 0) tiles_prefix_warp(p.walk, pts, kept);
+  pdl_launch_dependents();
   if (threadIdx.x == 32) {
     for (int s = 0; s < kQStages; ++s) {
       mbar_init(&full[s], 2);               // the leader's two loading warps
@@ -179,7 +180,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
   }
   __syncthreads();
   const int total = pts[p.walk.N];
-  if (cid >= total) return;                 // same decision in both CTAs of the pair
+  if (cid >= total) {                       // same decision in both CTAs of the pair
+    pdl_wait_prerequisites();
+    return;
+  }
   if (warp == 1) {
     tmem_alloc_pair(tmem_holder, kQTmemCols);
     tmem_relinquish_pair();
@@ -188,6 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
   __syncthreads();
   cluster_sync();                           // the peer's barriers exist before any remote use
   tc_fence_after();
+  pdl_wait_prerequisites();                 // the rows are there (the counts are the caller's)
   const uint32_t tmem_base = *tmem_holder;
   const uint32_t full_lead = map_to_rank(smem_u32(full), 0);
   const uint32_t sfull_lead = map_to_rank(smem_u32(sfull), 0);
@@ -581,9 +586,8 @@ cudaError_t run_q8(const void* rows, const void* weights, const Q8Params& p, int
   cudaError_t e = ensure_smem_limit(
       reinterpret_cast<const void*>(&expert_gemm_q8_kernel<kHidden>), smem, smem_set);
   if (e != cudaSuccess) return e;
-  expert_gemm_q8_kernel<kHidden>
-      <<<(num_sms / 2) * 2, kQThreads, smem, st>>>(maps, p);
-  return cudaGetLastError();
+  return launch_dependent(expert_gemm_q8_kernel<kHidden>, (num_sms / 2) * 2, kQThreads, smem, st, maps,
+                          p);
 }
 
 }  // namespace

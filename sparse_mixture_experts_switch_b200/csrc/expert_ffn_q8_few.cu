@@ -276,16 +276,8 @@ cudaError_t launch_expert_ffn_q8_few(const FfnQ8Args& a, cudaStream_t st) {
   p2.w = a.w2q;
   p2.wsc = a.w2s;
   p2.y = static_cast<__nv_bfloat16*>(a.y);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid((a.d + 15) / 16));
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_gemm_kernel<false, 1, 8>, p2);
+  return launch_dependent(few_gemm_kernel<false, 1, 8>, static_cast<int>(grid((a.d + 15) / 16)), 256,
+                          0, st, p2);
 }
 
 }  // namespace smoe

@@ -523,17 +523,8 @@ cudaError_t run_backward(const NormBwdArgs& a, cudaStream_t st) {
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.dgain == nullptr) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.d + 31) / 32));
-  cfg.blockDim = dim3(1024);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gain_reduce_kernel, nparts, a.d,
-                            static_cast<const float*>(a.part), a.dgain);
+  return launch_dependent(gain_reduce_kernel, (a.d + 31) / 32, 1024, 0, st, nparts, a.d, a.part,
+                          a.dgain);
 }
 
 }  // namespace

@@ -88,6 +88,27 @@ __device__ __forceinline__ uint4 q8_decode8(uint2 q, uint32_t byte) {
 
 // ---------------------------------------------------------------- launches
 
+// Launch as a programmatic dependent of the kernel before it on the stream: it
+// may take its place while that one ends, and waits (pdl_wait_prerequisites,
+// before anything that depends on earlier kernels of the same call, and before
+// leaving) until it and all before it are complete.  Never the first kernel of
+// a call: what the caller ran before is then complete.
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), int grid, int block, size_t smem,
+                                    cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Residual norm (norm.cu).
 struct NormArgs {
   int64_t T;

@@ -82,6 +82,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
   const int kstages = (kblocks + 1) / 2;
 
   if (warp == 0) tiles_prefix_warp(p.walk, pts, kept);
+  pdl_launch_dependents();
   if (threadIdx.x == 32) {
     for (int s = 0; s < kRStages; ++s) {
       mbar_init(&full[s], 2);               // the leader's two loading warps
@@ -97,7 +98,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
   }
   __syncthreads();
   const int total = pts[p.walk.N];
-  if (cid >= total) return;                 // same decision in both CTAs of the pair
+  if (cid >= total) {                       // same decision in both CTAs of the pair
+    pdl_wait_prerequisites();
+    return;
+  }
   if (warp == 1) {
     tmem_alloc_pair(tmem_holder, 512);
     tmem_relinquish_pair();
@@ -106,6 +110,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
   __syncthreads();
   cluster_sync();                           // the peer's barriers exist before any remote use
   tc_fence_after();
+  pdl_wait_prerequisites();                 // the rows are there (the counts are the caller's)
   const uint32_t tmem_base = *tmem_holder;
   const uint32_t full_lead = map_to_rank(smem_u32(full), 0);
   const uint32_t tempty_lead = map_to_rank(smem_u32(tempty), 0);
@@ -366,9 +371,8 @@ cudaError_t run_rows(const RowsGemmArgs& a, cudaStream_t st) {
   cudaError_t e = ensure_smem_limit(
       reinterpret_cast<const void*>(&rows_gemm_kernel<kMode, kWMN, kForward>), smem, smem_set);
   if (e != cudaSuccess) return e;
-  rows_gemm_kernel<kMode, kWMN, kForward>
-      <<<(a.num_sms / 2) * 2, kRThreads, smem, st>>>(maps, p);
-  return cudaGetLastError();
+  return launch_dependent(rows_gemm_kernel<kMode, kWMN, kForward>, (a.num_sms / 2) * 2, kRThreads,
+                          smem, st, maps, p);
 }
 
 }  // namespace

@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(
     int64_t rows, int cols, const uint4* __restrict__ src, const int* __restrict__ counts,
     int64_t C, const int* __restrict__ slot_token, int64_t T, uint4* __restrict__ copy,
     uint8_t* __restrict__ q, uint8_t* __restrict__ s, DevErr* err) {
+  pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int nv = cols / 8;
   const int nv_up = (nv + 31) / 32 * 32;
@@ -91,6 +92,8 @@ __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(
     int64_t rows, int cols, const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
     const int* __restrict__ counts, int64_t C, uint4* __restrict__ out,
     uint8_t* __restrict__ mask) {
+  pdl_launch_dependents();
+  pdl_wait_prerequisites();                          // (launched after another kernel of the call)
   const int lane = threadIdx.x & 31;
   const int nv = cols / 8;
   const int64_t nblk = q8_blocks(cols);
@@ -120,6 +123,7 @@ __global__ void __launch_bounds__(kThreads) gather_rows_q8_kernel(
     const uint8_t* __restrict__ xs, const int* __restrict__ counts, int64_t C, int64_t T,
     uint8_t* __restrict__ q, uint32_t* __restrict__ xw, int hcols, uint32_t* __restrict__ hw,
     DevErr* err) {
+  pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int nv = cols / 16;
   const int nblk = static_cast<int>(q8_blocks(cols));
@@ -228,12 +232,14 @@ cudaError_t launch_unpack_rows(int64_t rows, int cols, const uint8_t* q, const u
   auto* o = static_cast<uint4*>(out);
   auto* m = reinterpret_cast<uint8_t*>(mask);
   const int g = row_blocks(rows);
+  // first in its call (pad; with the mask), or after other kernels of it
   if (pad)
     unpack_rows_kernel<true, false><<<g, kThreads, 0, st>>>(rows, cols, q, s, counts, C, o, nullptr);
   else if (mask != nullptr)
     unpack_rows_kernel<false, true><<<g, kThreads, 0, st>>>(rows, cols, q, s, counts, C, o, m);
   else
-    unpack_rows_kernel<false, false><<<g, kThreads, 0, st>>>(rows, cols, q, s, counts, C, o, nullptr);
+    return launch_dependent(unpack_rows_kernel<false, false>, g, kThreads, 0, st, rows, cols, q, s,
+                            counts, C, o, m);
   return cudaGetLastError();
 }
 

@@ -82,7 +82,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   const int ncl = static_cast<int>(cluster_count_x());
   const long long lim = p.spin;
   const int total = p.N * p.tm * p.tn;
-  if (cid >= total) return;                 // same decision in both CTAs of the pair
+  pdl_launch_dependents();
+  if (cid >= total) {                       // same decision in both CTAs of the pair
+    pdl_wait_prerequisites();
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kGStages; ++s) {
@@ -106,6 +110,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   __syncthreads();
   cluster_sync();                           // the peer's barriers exist before any remote use
   tc_fence_after();
+  pdl_wait_prerequisites();                 // both operands are there
   const uint32_t tmem_base = *tmem_holder;
   const uint32_t full_lead = map_to_rank(smem_u32(full), 0);
   const uint32_t tail_own = map_to_rank(smem_u32(tail), rank);
@@ -355,8 +360,8 @@ cudaError_t launch_weight_grad(const WeightGradArgs& a, cudaStream_t st) {
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(&weight_grad_kernel), kGSmem,
                                     smem_set);
   if (e != cudaSuccess) return e;
-  weight_grad_kernel<<<(a.num_sms / 2) * 2, kGThreads, kGSmem, st>>>(ta, tb, to, p);
-  return cudaGetLastError();
+  return launch_dependent(weight_grad_kernel, (a.num_sms / 2) * 2, kGThreads, kGSmem, st, ta, tb, to,
+                          p);
 }
 
 }  // namespace smoe
