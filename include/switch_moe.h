@@ -475,8 +475,10 @@ switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
  *   the smallest e4m3 value, 2^-9 times its scale), so hq > 0 is the ReLU's
  *   mask.
  * y is switch_expert_ffn's.  Rows r >= n_e of all outputs are left untouched.
- * x, slot_token and SWITCH_FLAG_ROWS_DISPATCHED as for switch_expert_ffn (the
- * rows are always copied: SWITCH_FLAG_GATHER_IN_GEMM has no effect).
+ * x, slot_token and SWITCH_FLAG_ROWS_DISPATCHED as for switch_expert_ffn; the
+ * flags that choose its GEMM kernels have no effect (the rows are always copied,
+ * the products run on CTA pairs).  A token of a kept slot outside [0, T) sets
+ * SWITCH_ERR_DEVICE_BOUNDS (its row counts as zeros).
  * cfg->dtype SWITCH_BF16 only; workspace switch_workspace_size(). */
 switch_status_t switch_expert_ffn_checkpoint(const switch_config_t* cfg, const void* x,
                                              const int32_t* slot_token, const int32_t* counts,
@@ -492,7 +494,7 @@ switch_status_t switch_expert_ffn_checkpoint(const switch_config_t* cfg, const v
  *   dx [N, C, d_model], dw1 [N, d_ff, d_model], dw2 [N, d_model, d_ff] bf16.
  * Rows r >= n_e of the inputs may hold anything, those of dx are left
  * untouched; an expert without tokens has zero weight gradients.  fp32 sums, da
- * rounded once to bf16.  cfg->dtype SWITCH_BF16 only; workspace
+ * rounded once to bf16; the flags that choose GEMM kernels have no effect.  cfg->dtype SWITCH_BF16 only; workspace
  * switch_backward_workspace_size(). */
 switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const void* xq,
                                               const void* x_scale, const void* hq,

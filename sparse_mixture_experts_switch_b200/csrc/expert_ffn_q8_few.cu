@@ -1,9 +1,10 @@
-// The 8-bit expert FFNs (expert_ffn_q8.cu) for few tokens, as a decoding step has
-// them: no expert can hold more than kFewTokens.  Every weight byte is then used
-// for a handful of products, so the two products are streams of weights, bound
-// by memory: no tiles in shared memory and no TMEM, but weight rows loaded
-// straight into the registers of warp-level MMAs (m16n8k32, e4m3, fp32 sums): 16
-// features x 8 tokens a warp.
+// The 8-bit expert FFNs (expert_ffn_q8.cu) for the few tokens of a decoding step.
+// Every weight byte is then used for a handful of products, so the two products
+// are streams of weights, bound by memory and its latency: no tiles in shared
+// memory and no TMEM, but weight rows loaded straight into the registers of
+// warp-level MMAs (m16n8k32, e4m3, fp32 sums): 16 features x 8 tokens a warp (an
+// expert with more rows, which only rows dispatched by other means can be, takes
+// them eight at a time).
 //
 // A lane loads 16 consecutive bytes of a row, so a quad reads 64 and the order of
 // the columns inside an MMA differs from memory's: a sum does not mind, as long
@@ -18,6 +19,10 @@
 //     flight before it waits for the hidden rows.
 // Two CTAs an SM walk over the items of the experts that hold tokens, each with
 // the next item's weights in flight while the present one's sums are joined.
+//
+// Measured, calls back to back: 8 tokens of 8 of 128 experts of 1024 x 4096 (67
+// MB of weights, 10.3 us at the copy rate) 24.3 us, one token of one expert (8.4
+// MB) 14.4 us: two launches and three dependent loads each before the first MMA.
 #include "q8.cuh"
 
 namespace smoe {

@@ -1112,7 +1112,7 @@ switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
   a.spin = c.spin;
   a.num_sms = c.num_sms;
   a.xq = static_cast<const uint8_t*>(xq);
-  if (std::min(a.A, c.C) <= kFewTokens) {
+  if (a.A <= kFewTokens) {
     a.xs = static_cast<const uint8_t*>(x_scale);
     a.slot_token = dispatched ? nullptr : slot_token;
     return cuda_status(launch_expert_ffn_q8_few(a, c.st));

@@ -280,7 +280,18 @@ def switch_ep_experts(cfg, ep_, w1_local, w2_local, recv, out_peers, ws, stream=
 
 # ------------------------------------------------- norm and 8-bit rows
 # 8-bit rows are float8_e4m3fn values [rows, cols] with float8_e8m0fnu scales
-# [rows, ceil(cols / 128)] (tensors of any one-byte type are taken).
+# [rows, ceil(cols / 128)] (tensors of any one-byte type are taken).  A call runs on
+# the current device, which must be its tensors'.
+
+def _ps(*tensors):
+    """Device pointers of tensors on the current device (None -> NULL)."""
+    ptrs = [_p(t) for t in tensors]
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors of another device than the current one")
+    return ptrs
+
 
 def switch_norm_workspace_size(cfg):
     n = c_size_t(0)
@@ -317,46 +328,47 @@ def q8_weights(n, rows, cols, device="cuda"):
 
 
 def switch_residual_norm(cfg, x, residual, gain, eps, z, y, yq, y_scale, rstd, stream=None):
-    _check(_lib.switch_residual_norm(ctypes.byref(cfg), _p(x), _p(residual), _p(gain), float(eps),
-                                     _p(z), _p(y), _p(yq), _p(y_scale), _p(rstd),
-                                     _stream(stream)), "switch_residual_norm")
+    x, residual, gain, z, y, yq, y_scale, rstd = _ps(x, residual, gain, z, y, yq, y_scale, rstd)
+    _check(_lib.switch_residual_norm(ctypes.byref(cfg), x, residual, gain, float(eps), z, y, yq,
+                                     y_scale, rstd, _stream(stream)), "switch_residual_norm")
 
 
 def switch_residual_norm_backward(cfg, z, gain, rstd, dy, dsum, dx, dgain, ws, stream=None):
-    _check(_lib.switch_residual_norm_backward(ctypes.byref(cfg), _p(z), _p(gain), _p(rstd), _p(dy),
-                                              _p(dsum), _p(dx), _p(dgain), _p(ws),
-                                              0 if ws is None else ws.numel(), _stream(stream)),
+    ws_bytes = 0 if ws is None else ws.numel()
+    _check(_lib.switch_residual_norm_backward(ctypes.byref(cfg),
+                                              *_ps(z, gain, rstd, dy, dsum, dx, dgain, ws),
+                                              ws_bytes, _stream(stream)),
            "switch_residual_norm_backward")
 
 
 def switch_quantize_weights(cfg, w1, w2, w1q, w1_scale, w2q, w2_scale, stream=None):
-    _check(_lib.switch_quantize_weights(ctypes.byref(cfg), _p(w1), _p(w2), _p(w1q), _p(w1_scale),
-                                        _p(w2q), _p(w2_scale), _stream(stream)),
-           "switch_quantize_weights")
+    _check(_lib.switch_quantize_weights(ctypes.byref(cfg),
+                                        *_ps(w1, w2, w1q, w1_scale, w2q, w2_scale),
+                                        _stream(stream)), "switch_quantize_weights")
 
 
 def switch_expert_ffn_q8(cfg, xq, x_scale, slot_token, counts, w1q, w1_scale, w2q, w2_scale, y, ws,
                          stream=None):
-    _check(_lib.switch_expert_ffn_q8(ctypes.byref(cfg), _p(xq), _p(x_scale), _p(slot_token),
-                                     _p(counts), _p(w1q), _p(w1_scale), _p(w2q), _p(w2_scale),
-                                     _p(y), _p(ws), ws.numel(), _stream(stream)),
+    _check(_lib.switch_expert_ffn_q8(ctypes.byref(cfg),
+                                     *_ps(xq, x_scale, slot_token, counts, w1q, w1_scale, w2q,
+                                          w2_scale, y, ws), ws.numel(), _stream(stream)),
            "switch_expert_ffn_q8")
 
 
 def switch_expert_ffn_checkpoint(cfg, x, slot_token, counts, w1, w2, y, xq, x_scale, hq, h_scale, ws,
                                  stream=None):
-    _check(_lib.switch_expert_ffn_checkpoint(ctypes.byref(cfg), _p(x), _p(slot_token), _p(counts),
-                                             _p(w1), _p(w2), _p(y), _p(xq), _p(x_scale), _p(hq),
-                                             _p(h_scale), _p(ws), ws.numel(), _stream(stream)),
+    _check(_lib.switch_expert_ffn_checkpoint(ctypes.byref(cfg),
+                                             *_ps(x, slot_token, counts, w1, w2, y, xq, x_scale, hq,
+                                                  h_scale, ws), ws.numel(), _stream(stream)),
            "switch_expert_ffn_checkpoint")
 
 
 def switch_expert_ffn_backward_q8(cfg, xq, x_scale, hq, h_scale, counts, w1, w2, dy, dx, dw1, dw2,
                                   ws, stream=None):
-    _check(_lib.switch_expert_ffn_backward_q8(ctypes.byref(cfg), _p(xq), _p(x_scale), _p(hq),
-                                              _p(h_scale), _p(counts), _p(w1), _p(w2), _p(dy),
-                                              _p(dx), _p(dw1), _p(dw2), _p(ws), ws.numel(),
-                                              _stream(stream)), "switch_expert_ffn_backward_q8")
+    _check(_lib.switch_expert_ffn_backward_q8(ctypes.byref(cfg),
+                                              *_ps(xq, x_scale, hq, h_scale, counts, w1, w2, dy, dx,
+                                                   dw1, dw2, ws), ws.numel(), _stream(stream)),
+           "switch_expert_ffn_backward_q8")
 
 
 def switch_checkpoint_size(cfg):
@@ -372,13 +384,15 @@ def checkpoint(cfg, device="cuda"):
 
 
 def switch_checkpoint_save(cfg, ws, ckpt, stream=None):
-    _check(_lib.switch_checkpoint_save(ctypes.byref(cfg), _p(ws), ws.numel(), _p(ckpt),
-                                       ckpt.numel(), _stream(stream)), "switch_checkpoint_save")
+    w, c = _ps(ws, ckpt)
+    _check(_lib.switch_checkpoint_save(ctypes.byref(cfg), w, ws.numel(), c, ckpt.numel(),
+                                       _stream(stream)), "switch_checkpoint_save")
 
 
 def switch_checkpoint_load(cfg, x, ckpt, ws, stream=None):
-    _check(_lib.switch_checkpoint_load(ctypes.byref(cfg), _p(x), _p(ckpt), ckpt.numel(), _p(ws),
-                                       ws.numel(), _stream(stream)), "switch_checkpoint_load")
+    x, c, w = _ps(x, ckpt, ws)
+    _check(_lib.switch_checkpoint_load(ctypes.byref(cfg), x, c, ckpt.numel(), w, ws.numel(),
+                                       _stream(stream)), "switch_checkpoint_load")
 
 
 def switch_get_device_error(ws, stream=None):
