@@ -258,6 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
             !mbar_wait_cluster(&full[s], (issued_phase >> s) & 1u, kCopyDrainCycles))
           report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereDrain, s);
     }
+    settle_copies(abort_flag);
   } else if (warp == 3) {
     // ------------------------------------------------------------- scales
     // Groups of 512 columns by asynchronous copies, as far ahead as the ring

@@ -14,6 +14,16 @@ constexpr float kQ8Least = 0.001953125f;               // 2^-9, the smallest e4m
 // takes microseconds).
 constexpr long long kCopyDrainCycles = 40000000LL;
 
+// After a failure the two CTAs of a pair may have issued different stages, and
+// the leader's barriers then do not tell of all of them: the loading warps stay
+// for a time in which every copy in flight lands (0.2 ms).
+__device__ __forceinline__ void settle_copies(const volatile int* abort_flag) {
+  if (*abort_flag == 0) return;
+  const long long t0 = clock64();
+  while (clock64() - t0 < 400000) {
+  }
+}
+
 // ok of all 128 threads of named barrier `id`.
 __device__ __forceinline__ bool all_of_barrier(bool ok, int id) {
   int r;

@@ -175,6 +175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereDrain, s);
       }
     }
+    settle_copies(abort_flag);
   } else if (warp == 3) {
     // ----------------------------------------- ragged stages: rows of no token
     int stage = 0;

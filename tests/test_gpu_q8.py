@@ -282,8 +282,89 @@ def test_ffn_q8_scale_range(sm):
         check(y[e, :n], want, tol, f"expert {e}")
 
 
-def test_bad_slot_token_is_reported(sm):
-    T, d, F, N = 20, 64, 64, 2
+def test_ffn_q8_many_experts(sm):
+    """As many experts as a config takes, most without tokens."""
+    T, d, F, N = 300, 64, 128, 1024
+    C, counts, slot, kept, x, w1, w2 = ffn_inputs(T, d, F, N, 8.0, 3, dead=range(0, 1024, 3))
+    xq, xs = ref.to_q8(x)
+    w1q, w1s = ref.as_q8(*ref.quantize_weights(w1))
+    w2q, w2s = ref.as_q8(*ref.quantize_weights(w2))
+    cfg = sm.config(T, d, F, N, 8.0)
+    ws = sm.workspace(cfg)
+    y = torch.full((N, C, d), -7.0, dtype=torch.bfloat16, device="cuda")
+    sm.switch_expert_ffn_q8(cfg, dev(xq), dev(xs), dev(slot), dev(counts), dev(w1q), dev(w1s),
+                            dev(w2q), dev(w2s), y, ws)
+    assert sm.switch_get_device_error(ws)[0] == 0
+    xv, w1v, w2v = ref.rows(xq, xs), ref.weights(w1q, w1s), ref.weights(w2q, w2s)
+    for e in range(N):
+        n = int(kept[e])
+        assert (y[e, n:] == -7).all()
+        if n:
+            want, tol = ffn_q8_want(xv[slot.view(N, C)[e, :n].long()], w1v[e], w2v[e])
+            check(y[e, :n], want, tol, f"expert {e}")
+
+
+@pytest.mark.parametrize("T", [3, 400])
+def test_ffn_q8_top2(sm, T):
+    """Both routes of a token in slots of their experts: capacity over 2 T assignments, the
+    same token's row twice."""
+    from oracle.switch_oracle import capacity
+    d, F, N, cf = 128, 320, 5, 1.0
+    C = capacity(2 * T, N, cf)
+    rng = np.random.default_rng(T)
+    pairs = np.array([rng.permutation(N)[:2] for _ in range(T)])
+    tok = [[t for t in range(T) if pairs[t, 0] == e] + [t for t in range(T) if pairs[t, 1] == e]
+           for e in range(N)]
+    counts = torch.tensor([len(t) for t in tok], dtype=torch.int32)
+    slot = torch.full((N, C), -1, dtype=torch.int32)
+    for e in range(N):
+        slot[e, :min(len(tok[e]), C)] = torch.tensor(tok[e][:C], dtype=torch.int32)
+    _, _, _, _, x, w1, w2 = ffn_inputs(T, d, F, N, cf, 17)
+    xq, xs = ref.to_q8(x)
+    w1q, w1s = ref.as_q8(*ref.quantize_weights(w1))
+    w2q, w2s = ref.as_q8(*ref.quantize_weights(w2))
+    cfg = sm.config(T, d, F, N, cf, flags=sm.FLAG_TOP2)
+    ws = sm.workspace(cfg)
+    y = torch.full((N, C, d), -7.0, dtype=torch.bfloat16, device="cuda")
+    sm.switch_expert_ffn_q8(cfg, dev(xq), dev(xs), dev(slot.reshape(-1)), dev(counts), dev(w1q),
+                            dev(w1s), dev(w2q), dev(w2s), y, ws)
+    assert sm.switch_get_device_error(ws)[0] == 0
+    xv, w1v, w2v = ref.rows(xq, xs), ref.weights(w1q, w1s), ref.weights(w2q, w2s)
+    for e in range(N):
+        n = min(len(tok[e]), C)
+        assert (y[e, n:] == -7).all()
+        if n:
+            want, tol = ffn_q8_want(xv[slot[e, :n].long()], w1v[e], w2v[e])
+            check(y[e, :n], want, tol, f"expert {e}")
+
+
+def test_ffn_q8_more_rows_than_tokens(sm):
+    """Rows dispatched by other means: a config of few tokens whose capacity holds more rows
+    (the few-token path takes an expert's rows eight at a time)."""
+    T, d, F, N, cf = 4, 192, 320, 2, 10.0
+    C = sm.switch_capacity(T, N, cf)
+    assert C == 20
+    _, _, _, _, _, w1, w2 = ffn_inputs(T, d, F, N, cf, 23)
+    x = torch.randn(N * C, d, generator=gen(2)).double()
+    counts = torch.tensor([19, 8], dtype=torch.int32)
+    xq, xs = ref.to_q8(x)
+    w1q, w1s = ref.as_q8(*ref.quantize_weights(w1))
+    w2q, w2s = ref.as_q8(*ref.quantize_weights(w2))
+    cfg = sm.config(T, d, F, N, cf, flags=sm.FLAG_ROWS_DISPATCHED)
+    ws = sm.workspace(cfg)
+    y = torch.full((N, C, d), -7.0, dtype=torch.bfloat16, device="cuda")
+    sm.switch_expert_ffn_q8(cfg, dev(xq), dev(xs), None, dev(counts), dev(w1q), dev(w1s), dev(w2q),
+                            dev(w2s), y, ws)
+    xv, w1v, w2v = ref.rows(xq, xs), ref.weights(w1q, w1s), ref.weights(w2q, w2s)
+    for e, n in enumerate(counts.tolist()):
+        assert (y[e, n:] == -7).all()
+        want, tol = ffn_q8_want(xv.view(N, C, d)[e, :n], w1v[e], w2v[e])
+        check(y[e, :n], want, tol, f"expert {e}")
+
+
+@pytest.mark.parametrize("T", [7, 90])
+def test_bad_slot_token_is_reported(sm, T):
+    d, F, N = 64, 64, 2
     C, counts, slot, kept, x, w1, w2 = ffn_inputs(T, d, F, N, 2.0, 9)
     slot[0] = T + 5
     xq, xs = ref.to_q8(x)
@@ -318,10 +399,42 @@ def test_ffn_q8_forced_timeout_reports_and_recovers(sm):
     assert s1 == 0 and s2 == 0 and torch.equal(y1, y2)
 
 
+def test_checkpoint_forced_timeouts_report_and_recover(sm):
+    """The same for the products of the FFN with checkpoint and of its backward."""
+    T, d, F, N = 64, 65536, 128, 1
+    C = sm.switch_capacity(T, N, 1.0)
+    g = gen(5)
+    flags = sm.FLAG_ROWS_DISPATCHED
+    x = dev(torch.randn(C, d, generator=g).bfloat16())
+    dy = dev(torch.randn(N, C, d, generator=g).bfloat16())
+    w1 = dev((torch.randn(N, F, d, generator=g) * 0.01).bfloat16())
+    w2 = dev((torch.randn(N, d, F, generator=g) * 0.01).bfloat16())
+    counts = torch.tensor([T - 3], dtype=torch.int32, device="cuda")
+
+    def run(spin):
+        cfg = sm.config(T, d, F, N, 1.0, flags=flags, spin_limit=spin)
+        ws = sm.backward_workspace(cfg)
+        q, s = sm.q8_rows(C, d)
+        hq, hs = sm.q8_rows(C, F)
+        y, dx = torch.zeros_like(dy), torch.zeros_like(dy)
+        dw1, dw2 = torch.zeros_like(w1), torch.zeros_like(w2)
+        sm.switch_expert_ffn_checkpoint(cfg, x, None, counts, w1, w2, y, q, s, hq, hs, ws)
+        first = sm.switch_get_device_error(ws)[0]
+        sm.switch_expert_ffn_backward_q8(cfg, q, s, hq, hs, counts, w1, w2, dy, dx, dw1, dw2, ws)
+        return first, sm.switch_get_device_error(ws)[0], (y, dx, dw1, dw2)
+
+    f, b, _ = run(1)
+    assert f == 5 and b == 5
+    (f1, b1, one), (f2, b2, two) = run(0), run(0)
+    assert f1 == b1 == f2 == b2 == 0
+    assert all(torch.equal(u, v) for u, v in zip(one, two))
+
+
 # ------------------------------------------------------------ checkpoints
 
 CKPT = [(1, 64, 64, 1, 1.0, ()), (300, 64, 128, 2, 1.0, ()), (700, 320, 832, 6, 1.25, (2,)),
-        (513, 192, 320, 3, 2.0, ()), (1000, 512, 1024, 4, 0.5, (0,)), (129, 128, 256, 1, 1.0, ())]
+        (513, 192, 320, 3, 2.0, ()), (1000, 512, 1024, 4, 0.5, (0,)), (129, 128, 256, 1, 1.0, ()),
+        (200, 64, 64, 1000, 8.0, tuple(range(0, 1000, 3)))]
 
 
 @pytest.mark.parametrize("T,d,F,N,cf,dead", CKPT)
