@@ -209,6 +209,14 @@ __device__ __forceinline__ void tma_prefetch_l2_2d(const CUtensorMap* map, int c
                : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* map, int c0, int c1, int c2,
+                                                   int c3) {
+  asm volatile(
+      "cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map),
+      "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
 // 16-byte asynchronous global -> shared copy (L2 only), and the mbarrier
 // arrival that fires once every earlier cp.async of this thread has landed.
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {

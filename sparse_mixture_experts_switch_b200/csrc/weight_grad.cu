@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kGK = 64;                                // rows of a stage
 constexpr int kGStages = 5;
+constexpr int kGAhead = 2;                             // tiles of a pair between prefetch and load
 constexpr uint32_t kGOpBytes = 128 * kGK * 2;          // 16 KB: 64 rows x 128 columns
 constexpr uint32_t kGStageBytes = 2 * kGOpBytes;
 constexpr int kGDrainWarps = 16;
@@ -162,6 +163,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         if (++stage == kGStages) { stage = 0; phase ^= 1u; }
       }
       if (!ok) break;
+      // the operands of a later tile into L2: of the tiles that share one, the
+      // first asks for it
+      const int ahead = tile + kGAhead * ncl;
+      if (ahead < total) {
+        const GradTile u = grad_tile(p, ahead);
+        if ((is_b ? u.m0 : u.n0) == 0 && elect_one()) {
+          const int xu = ((is_b ? u.n0 : u.m0) + static_cast<int>(rank) * 128) >> 6;
+          for (int kb = 0; kb < u.kblocks; ++kb) tma_prefetch_l2_4d(map, 0, kb * kGK, xu, u.e);
+        }
+      }
     }
     // Never leave with copies in flight into the pair's shared memory: ragged
     // stages on this CTA's barriers, the others on the leader's.  (After a failure
