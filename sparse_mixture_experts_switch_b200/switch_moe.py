@@ -135,8 +135,14 @@ def _p(t):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object (3 us of a call's host time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -285,11 +291,21 @@ def switch_ep_experts(cfg, ep_, w1_local, w2_local, recv, out_peers, ws, stream=
 
 def _ps(*tensors):
     """Device pointers of tensors on the current device (None -> NULL)."""
-    ptrs = [_p(t) for t in tensors]
-    dev = torch.cuda.current_device()
+    ptrs, dev = [], None
     for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors of another device than the current one")
+        if t is None:
+            ptrs.append(None)
+            continue
+        d = t.get_device()                   # -1: not a device tensor
+        if d != dev:
+            if d < 0:
+                raise ValueError("device tensors only: the library reads device memory")
+            if d != torch.cuda.current_device():
+                raise ValueError("tensors of another device than the current one")
+            dev = d
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        ptrs.append(t.data_ptr())
     return ptrs
 
 
