@@ -62,6 +62,7 @@ struct WeightGradArgs {
   const int* counts;
   const void *a, *b;
   void* dw;
+  bool last_first;           // experts from the last on
   DevErr* err;
   long long spin;
   int num_sms;

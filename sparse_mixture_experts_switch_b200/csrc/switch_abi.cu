@@ -1216,6 +1216,7 @@ switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const 
   g.a = dy;
   g.b = hb;
   g.dw = dw2;
+  g.last_first = true;                       // h's end is still in L2
   SMOE_TRY(launch_weight_grad(g, c.st));
   RowsGemmArgs a = rows_args(cfg, c, counts);
   a.n_out = F;
@@ -1239,6 +1240,7 @@ switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const 
   g.a = c.ws + c.L.da;
   g.b = xb;
   g.dw = dw1;
+  g.last_first = false;                      // dx read da's beginning last
   return cuda_status(launch_weight_grad(g, c.st));
 }
 

@@ -34,6 +34,7 @@ static_assert(kGSmem <= 232448, "a CTA's shared memory");
 
 struct GradParams {
   int N, M, Nn, tm, tn;      // tm, tn: 256-wide tiles
+  int last_first;            // experts from the last on
   int64_t C;
   const int* counts;
   DevErr* err;
@@ -44,12 +45,15 @@ struct GradTile {
   int e, m0, n0, kept, kblocks;
 };
 
-// Tile t: an expert's m tiles vary fastest, then its n tiles.
+// Tile t: an expert's m tiles vary fastest, then its n tiles.  The experts in
+// order, or from the last on: b has then just been written in order, and its end
+// is what L2 still holds.
 __device__ __forceinline__ GradTile grad_tile(const GradParams& p, int t) {
   GradTile r;
   const int per = p.tm * p.tn;
   r.e = t / per;
   const int local = t - r.e * per;
+  if (p.last_first) r.e = p.N - 1 - r.e;
   const int n = local / p.tm;
   r.n0 = n * 256;
   r.m0 = (local - n * p.tm) * 256;
@@ -361,6 +365,7 @@ cudaError_t launch_weight_grad(const WeightGradArgs& a, cudaStream_t st) {
   p.N = a.N;
   p.M = a.M;
   p.Nn = a.Nn;
+  p.last_first = a.last_first ? 1 : 0;
   p.tm = (a.M + 255) / 256;
   p.tn = (a.Nn + 255) / 256;
   p.C = a.C;
