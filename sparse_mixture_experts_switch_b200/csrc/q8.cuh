@@ -154,12 +154,17 @@ cudaError_t launch_quantize_rows(int64_t rows, int cols, const void* src, const 
                                  int64_t C, const int* slot_token, int64_t T, void* copy,
                                  bool positive, uint8_t* q, uint8_t* s, DevErr* err,
                                  cudaStream_t st);
-// bf16 rows from 8-bit rows of expert slots (kept rows only).  mask: also a bit
-// per value, set where the code is above zero [rows, cols / 32]; pad (without
-// mask): also zeros in the rows up to the next multiple of 64 (or C).
-cudaError_t launch_unpack_rows(int64_t rows, int cols, const uint8_t* q, const uint8_t* s,
-                               const int* counts, int64_t C, void* out, uint32_t* mask, bool pad,
-                               cudaStream_t st);
+// bf16 rows from one or two sets of 8-bit rows of expert slots (kept rows only).
+// pad: also zeros in the rows up to the next multiple of 64 (or C); else, with a
+// mask, a bit per value, set where the code is above zero [rows, cols / 32].
+struct UnpackSet {
+  int cols;
+  const uint8_t *q, *s;
+  void* out;
+  uint32_t* mask;
+};
+cudaError_t launch_unpack_rows(int64_t rows, const int* counts, int64_t C, bool pad,
+                               const UnpackSet* sets, int n, cudaStream_t st);
 // 8-bit rows into the slots of their experts (kept slots only; q null: the
 // rows are there already, xq and xs are the slots'), their scales as words
 // xw [ceil(cols / 512)][slots] (four blocks' bytes, 2^0 past the row's end),

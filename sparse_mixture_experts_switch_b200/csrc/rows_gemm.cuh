@@ -54,20 +54,21 @@ cudaError_t launch_rows_out(const RowsGemmArgs& a, cudaStream_t st);      // row
 cudaError_t launch_rows_da(const RowsGemmArgs& a, cudaStream_t st);       // (rows w) where mask
 cudaError_t launch_rows_dx(const RowsGemmArgs& a, cudaStream_t st);       // rows w
 
-// dw[e] [M, Nn] = a[e]^T b[e] over the kept rows of expert e (zeros without any);
-// a [N*C, M], b [N*C, Nn] bf16, what lies behind the kept rows is not used.
+// dw[g][e] [M, Nn] = a[g][e]^T b[g][e] over the kept rows of expert e (zeros
+// without any), for two gradients g; a [N*C, M], b [N*C, Nn] bf16, what lies
+// behind the kept rows is not used.
 struct WeightGradArgs {
-  int N, M, Nn;
+  int N;
+  int M[2], Nn[2];
   int64_t C;
   const int* counts;
-  const void *a, *b;
-  void* dw;
-  bool last_first;           // experts from the last on
+  const void *a[2], *b[2];
+  void* dw[2];
   DevErr* err;
   long long spin;
   int num_sms;
 };
-cudaError_t launch_weight_grad(const WeightGradArgs& a, cudaStream_t st);
+cudaError_t launch_weight_grads(const WeightGradArgs& a, cudaStream_t st);
 
 // bf16 [outer][k][m] as MN-major operand tiles (rows_gemm.cu).
 bool make_tmap_mn_major(CUtensorMap* map, const void* base, int64_t m, int64_t k, int64_t outer);

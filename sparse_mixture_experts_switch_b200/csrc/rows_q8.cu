@@ -88,17 +88,20 @@ __device__ __forceinline__ uint32_t flag_bits(uint32_t f) {
   return ((f >> 7) * 0x01020408u) >> 24;
 }
 
-// Zero rows up to the next multiple of 64 (kPad), or the kept rows' bits.
-template <bool kPad, bool kMask>
-__global__ void __launch_bounds__(kThreads) unpack_rows_kernel(
-    int64_t rows, int cols, const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
-    const int* __restrict__ counts, int64_t C, uint4* __restrict__ out,
-    uint8_t* __restrict__ mask) {
+// One set of rows per blockIdx.y.  kPad: zero rows up to the next multiple of 64;
+// else the kept rows' bits where there is a mask.
+template <bool kPad>
+__global__ void __launch_bounds__(kThreads) unpack_rows_kernel(int64_t rows,
+                                                              const int* __restrict__ counts,
+                                                              int64_t C, UnpackSet s0,
+                                                              UnpackSet s1) {
   pdl_launch_dependents();
-  pdl_wait_prerequisites();                          // (launched after another kernel of the call)
+  const UnpackSet u = blockIdx.y == 0 ? s0 : s1;
   const int lane = threadIdx.x & 31;
-  const int nv = cols / 8;
-  const int64_t nblk = q8_blocks(cols);
+  const int nv = u.cols / 8;
+  const int64_t nblk = q8_blocks(u.cols);
+  auto* out = static_cast<uint4*>(u.out);
+  auto* mask = reinterpret_cast<uint8_t*>(u.mask);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < rows;
        r += step) {
@@ -109,11 +112,11 @@ __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(
         for (int v = lane; v < nv; v += 32) out[r * nv + v] = make_uint4(0, 0, 0, 0);
       continue;
     }
-    const uint2* row = reinterpret_cast<const uint2*>(q + r * cols);
+    const uint2* row = reinterpret_cast<const uint2*>(u.q + r * u.cols);
     for (int v = lane; v < nv; v += 32) {
       const uint2 w = __ldg(row + v);
-      out[r * nv + v] = q8_decode8(w, __ldg(s + r * nblk + v / 16));
-      if (kMask)
+      out[r * nv + v] = q8_decode8(w, __ldg(u.s + r * nblk + v / 16));
+      if (!kPad && mask != nullptr)
         mask[r * nv + v] = static_cast<uint8_t>(flag_bits(positive_codes(w.x)) |
                                                 flag_bits(positive_codes(w.y)) << 4);
     }
@@ -227,21 +230,15 @@ cudaError_t launch_quantize_rows(int64_t rows, int cols, const void* src, const 
   return cudaGetLastError();
 }
 
-cudaError_t launch_unpack_rows(int64_t rows, int cols, const uint8_t* q, const uint8_t* s,
-                               const int* counts, int64_t C, void* out, uint32_t* mask, bool pad,
-                               cudaStream_t st) {
+cudaError_t launch_unpack_rows(int64_t rows, const int* counts, int64_t C, bool pad,
+                               const UnpackSet* sets, int n, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  auto* o = static_cast<uint4*>(out);
-  auto* m = reinterpret_cast<uint8_t*>(mask);
-  const int g = row_blocks(rows);
-  // first in its call (pad; with the mask), or after other kernels of it
+  const dim3 grid(static_cast<unsigned>(row_blocks(rows)), static_cast<unsigned>(n));
+  const UnpackSet& last = sets[n - 1];
   if (pad)
-    unpack_rows_kernel<true, false><<<g, kThreads, 0, st>>>(rows, cols, q, s, counts, C, o, nullptr);
-  else if (mask != nullptr)
-    unpack_rows_kernel<false, true><<<g, kThreads, 0, st>>>(rows, cols, q, s, counts, C, o, m);
+    unpack_rows_kernel<true><<<grid, kThreads, 0, st>>>(rows, counts, C, sets[0], last);
   else
-    return launch_dependent(unpack_rows_kernel<false, false>, g, kThreads, 0, st, rows, cols, q, s,
-                            counts, C, o, m);
+    unpack_rows_kernel<false><<<grid, kThreads, 0, st>>>(rows, counts, C, sets[0], last);
   return cudaGetLastError();
 }
 

@@ -1199,25 +1199,12 @@ switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const 
   uint8_t* xb = c.ws + c.L.xdisp;
   uint8_t* hb = c.ws + c.L.hbuf;
   uint32_t* mask = c.at<uint32_t>(c.L.mask);
-  SMOE_TRY(launch_unpack_rows(S, F, static_cast<const uint8_t*>(hq),
-                              static_cast<const uint8_t*>(h_scale), counts, c.C, hb, mask, false,
-                              c.st));
-  // dw2 = dy^T h while h is fresh, da = (dy w2) where h > 0, dx = da w1,
-  // dw1 = da^T x
-  WeightGradArgs g{};
-  g.N = cfg->n_experts;
-  g.C = c.C;
-  g.counts = counts;
-  g.err = c.err;
-  g.spin = c.spin;
-  g.num_sms = c.num_sms;
-  g.M = d;
-  g.Nn = F;
-  g.a = dy;
-  g.b = hb;
-  g.dw = dw2;
-  g.last_first = true;                       // h's end is still in L2
-  SMOE_TRY(launch_weight_grad(g, c.st));
+  const UnpackSet sets[2] = {{F, static_cast<const uint8_t*>(hq),
+                              static_cast<const uint8_t*>(h_scale), hb, mask},
+                             {d, static_cast<const uint8_t*>(xq),
+                              static_cast<const uint8_t*>(x_scale), xb, nullptr}};
+  SMOE_TRY(launch_unpack_rows(S, counts, c.C, false, sets, 2, c.st));
+  // da = (dy w2) where h > 0, dx = da w1, dw1 = da^T x, dw2 = dy^T h
   RowsGemmArgs a = rows_args(cfg, c, counts);
   a.n_out = F;
   a.K = d;
@@ -1232,16 +1219,24 @@ switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const 
   a.w = w1;
   a.out = dx;
   SMOE_TRY(launch_rows_dx(a, c.st));
-  SMOE_TRY(launch_unpack_rows(S, d, static_cast<const uint8_t*>(xq),
-                              static_cast<const uint8_t*>(x_scale), counts, c.C, xb, nullptr,
-                              false, c.st));
-  g.M = F;
-  g.Nn = d;
-  g.a = c.ws + c.L.da;
-  g.b = xb;
-  g.dw = dw1;
-  g.last_first = false;                      // dx read da's beginning last
-  return cuda_status(launch_weight_grad(g, c.st));
+  WeightGradArgs g{};
+  g.N = cfg->n_experts;
+  g.C = c.C;
+  g.counts = counts;
+  g.err = c.err;
+  g.spin = c.spin;
+  g.num_sms = c.num_sms;
+  g.M[0] = F;
+  g.Nn[0] = d;
+  g.a[0] = c.ws + c.L.da;
+  g.b[0] = xb;
+  g.dw[0] = dw1;
+  g.M[1] = d;
+  g.Nn[1] = F;
+  g.a[1] = dy;
+  g.b[1] = hb;
+  g.dw[1] = dw2;
+  return cuda_status(launch_weight_grads(g, c.st));
 }
 
 // What switch_layer_forward (SWITCH_FLAG_TRAINING) keeps, outside the
@@ -1321,9 +1316,8 @@ switch_status_t switch_checkpoint_load(const switch_config_t* cfg, const void* x
                            cudaMemcpyDeviceToDevice, c.st));
   SMOE_TRY(launch_gather_rows(S, static_cast<int64_t>(cfg->d_model) * 2,
                               c.at<int>(c.L.slot_token), x, c.ws + c.L.xdisp, c.st));
-  return cuda_status(launch_unpack_rows(S, cfg->d_ff, in + k.hq, in + k.hs,
-                                        c.at<int>(c.L.counts), c.C, c.ws + c.L.hbuf, nullptr,
-                                        true, c.st));
+  const UnpackSet h{cfg->d_ff, in + k.hq, in + k.hs, c.ws + c.L.hbuf, nullptr};
+  return cuda_status(launch_unpack_rows(S, c.at<int>(c.L.counts), c.C, true, &h, 1, c.st));
 }
 
 switch_status_t switch_get_device_error(void* ws, void* stream, int32_t* where_out,

@@ -2,6 +2,8 @@
 //
 //   dw[e][m, n] = sum over the kept rows r of expert e of a[r, m] b[r, n]
 //
+// of two such gradients (of both weights) in one launch.
+//
 // A product with a short sum (an expert's few hundred rows) and a large result:
 // bound by writing dw.  One persistent kernel on CTA pairs, 256 x 256 tiles; both
 // operands lie with m or n contiguous and are used as they lie (MN-major tiles,
@@ -37,9 +39,13 @@ constexpr uint32_t kGBoxBytes = 32 * 128;              // 32 rows x 64 bf16
 constexpr uint32_t kGSmem = 1024 + kGStages * kGStageBytes + kGDrainWarps * kGBoxBytes + 256;
 static_assert(kGSmem <= 232448, "a CTA's shared memory");
 
+struct GradMaps {
+  CUtensorMap a[2], b[2], out[2];
+};
 struct GradParams {
-  int N, M, Nn, tm, tn;      // tm, tn: 256-wide tiles
-  int last_first;            // experts from the last on
+  int N;
+  int M[2], Nn[2], tm[2], tn[2];   // tm, tn: 256-wide tiles
+  int total[2];                    // tiles of the first gradient, of both
   int64_t C;
   const int* counts;
   DevErr* err;
@@ -47,21 +53,22 @@ struct GradParams {
 };
 
 struct GradTile {
-  int e, m0, n0, kept, kblocks;
+  int g, e, m0, n0, kept, kblocks;
 };
 
-// Tile t: an expert's m tiles vary fastest, then its n tiles.  The experts in
-// order, or from the last on: b has then just been written in order, and its end
-// is what L2 still holds.
+// Tile t: first the tiles of gradient 0, then those of gradient 1; an expert's m
+// tiles vary fastest, then its n tiles.
 __device__ __forceinline__ GradTile grad_tile(const GradParams& p, int t) {
   GradTile r;
-  const int per = p.tm * p.tn;
+  r.g = t < p.total[0] ? 0 : 1;
+  if (r.g) t -= p.total[0];
+  const int tm = r.g ? p.tm[1] : p.tm[0];
+  const int per = tm * (r.g ? p.tn[1] : p.tn[0]);
   r.e = t / per;
   const int local = t - r.e * per;
-  if (p.last_first) r.e = p.N - 1 - r.e;
-  const int n = local / p.tm;
+  const int n = local / tm;
   r.n0 = n * 256;
-  r.m0 = (local - n * p.tm) * 256;
+  r.m0 = (local - n * tm) * 256;
   const int64_t c = __ldg(p.counts + r.e);
   r.kept = static_cast<int>(c < 0 ? 0 : (c < p.C ? c : p.C));
   r.kblocks = (r.kept + kGK - 1) / kGK;
@@ -69,9 +76,7 @@ __device__ __forceinline__ GradTile grad_tile(const GradParams& p, int t) {
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
-    weight_grad_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                       const __grid_constant__ CUtensorMap tmap_b,
-                       const __grid_constant__ CUtensorMap tmap_out, GradParams p) {
+    weight_grad_kernel(const __grid_constant__ GradMaps maps, GradParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -91,7 +96,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   const int cid = static_cast<int>(cluster_id_x());
   const int ncl = static_cast<int>(cluster_count_x());
   const long long lim = p.spin;
-  const int total = p.N * p.tm * p.tn;
+  const int total = p.total[1];
   pdl_launch_dependents();
   if (cid >= total) {                       // same decision in both CTAs of the pair
     pdl_wait_prerequisites();
@@ -129,8 +134,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   if (warp == 0 || warp == 2) {
     // ------------------------------------------- TMA: warp 0 A, warp 2 B
     const bool is_b = warp == 2;
-    const CUtensorMap* map = is_b ? &tmap_b : &tmap_a;
-    if (elect_one()) tma_prefetch_desc(map);
+    const CUtensorMap* map0 = is_b ? maps.b : maps.a;
+    if (elect_one()) tma_prefetch_desc(map0);
     int stage = 0;
     uint32_t phase = 0;
     uint32_t full_mask = 0, tail_mask = 0, full_phase = 0, tail_phase = 0;
@@ -138,6 +143,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     for (int tile = cid; tile < total; tile += ncl) {
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       const GradTile t = grad_tile(p, tile);
+      const CUtensorMap* map = map0 + t.g;
       const int x = (is_b ? t.n0 : t.m0) + static_cast<int>(rank) * 128;
       bool ok = true;
       for (int kb = 0; kb < t.kblocks; ++kb) {
@@ -179,7 +185,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         const GradTile u = grad_tile(p, ahead);
         if ((is_b ? u.m0 : u.n0) == 0 && elect_one()) {
           const int xu = ((is_b ? u.n0 : u.m0) + static_cast<int>(rank) * 128) >> 6;
-          for (int kb = 0; kb < u.kblocks; ++kb) tma_prefetch_l2_4d(map, 0, kb * kGK, xu, u.e);
+          for (int kb = 0; kb < u.kblocks; ++kb)
+            tma_prefetch_l2_4d(map0 + u.g, 0, kb * kGK, xu, u.e);
         }
       }
     }
@@ -288,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     const int cg = (warp - 4) >> 2;         // 64 of the tile's columns
     const uint32_t box = smem_u32(stage_out + (warp - 4) * kGBoxBytes);
     const uint32_t swz = static_cast<uint32_t>(lane & 7);
-    if (lane == 0) tma_prefetch_desc(&tmap_out);
+    if (lane == 0) tma_prefetch_desc(&maps.out[0]);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = cid; tile < total; tile += ncl) {
@@ -304,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const GradTile t = grad_tile(p, tile);
       const int m = t.m0 + static_cast<int>(rank) * 128 + q * 32;
       const int n = t.n0 + cg * 64;
-      const bool on = m < p.M && n < p.Nn;  // warp-uniform: the box begins inside dw
+      const bool on = m < p.M[t.g] && n < p.Nn[t.g];   // warp-uniform: the box begins inside dw
       uint32_t pk[32];
       if (on) {
         if (t.kblocks > 0) {
@@ -341,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d(&tmap_out, box, n, m, t.e);
+          tma_store_3d(&maps.out[t.g], box, n, m, t.e);
           bulk_commit();
         }
       }
@@ -360,30 +367,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_weight_grad(const WeightGradArgs& a, cudaStream_t st) {
-  CUtensorMap ta, tb, to;
-  bool ok = make_tmap_mn_major(&ta, a.a, a.M, a.C, a.N);
-  ok = ok && make_tmap_mn_major(&tb, a.b, a.Nn, a.C, a.N);
-  ok = ok && make_tmap_bf16_3d(&to, a.dw, a.Nn, a.M, a.N, 64, 32);
-  if (!ok) return cudaErrorInvalidValue;
+cudaError_t launch_weight_grads(const WeightGradArgs& a, cudaStream_t st) {
+  GradMaps maps;
   GradParams p{};
   p.N = a.N;
-  p.M = a.M;
-  p.Nn = a.Nn;
-  p.last_first = a.last_first ? 1 : 0;
-  p.tm = (a.M + 255) / 256;
-  p.tn = (a.Nn + 255) / 256;
   p.C = a.C;
   p.counts = a.counts;
   p.err = a.err;
   p.spin = a.spin;
-  if (static_cast<int64_t>(p.N) * p.tm * p.tn > INT32_MAX) return cudaErrorInvalidValue;
+  int64_t total = 0;
+  for (int g = 0; g < 2; ++g) {
+    bool ok = make_tmap_mn_major(&maps.a[g], a.a[g], a.M[g], a.C, a.N);
+    ok = ok && make_tmap_mn_major(&maps.b[g], a.b[g], a.Nn[g], a.C, a.N);
+    ok = ok && make_tmap_bf16_3d(&maps.out[g], a.dw[g], a.Nn[g], a.M[g], a.N, 64, 32);
+    if (!ok) return cudaErrorInvalidValue;
+    p.M[g] = a.M[g];
+    p.Nn[g] = a.Nn[g];
+    p.tm[g] = (a.M[g] + 255) / 256;
+    p.tn[g] = (a.Nn[g] + 255) / 256;
+    total += static_cast<int64_t>(a.N) * p.tm[g] * p.tn[g];
+    if (total > INT32_MAX) return cudaErrorInvalidValue;
+    p.total[g] = static_cast<int>(total);
+  }
   static size_t smem_set[64] = {};
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(&weight_grad_kernel), kGSmem,
                                     smem_set);
   if (e != cudaSuccess) return e;
-  return launch_dependent(weight_grad_kernel, (a.num_sms / 2) * 2, kGThreads, kGSmem, st, ta, tb, to,
-                          p);
+  return launch_dependent(weight_grad_kernel, (a.num_sms / 2) * 2, kGThreads, kGSmem, st, maps, p);
 }
 
 }  // namespace smoe
