@@ -1,8 +1,9 @@
 // Kernels that make, unpack and move 8-bit block rows (format: q8.cuh).  All
 // are one pass over memory: a warp takes a row, 8 bf16 (or 16 codes) a lane,
 // and 16 neighbouring lanes hold one block of 128 columns.  Measured alone at 25278
-// rows: unpacking 4096 columns with their bits 53 us (310 MB, 5.9 TB/s), copying
-// and quantising 1024 columns 23 us (129 MB), moving 1024 codes 14 us (52 MB).
+// rows: unpacking 4096 columns with their bits and 1024 columns 62 us (388 MB, 6.2
+// TB/s), copying and quantising 1024 columns 23 us (129 MB), moving 1024 codes 14 us
+// (52 MB).
 #include "q8.cuh"
 
 namespace smoe {
