@@ -494,8 +494,8 @@ switch_status_t switch_expert_ffn_checkpoint(const switch_config_t* cfg, const v
  *   dx [N, C, d_model], dw1 [N, d_ff, d_model], dw2 [N, d_model, d_ff] bf16.
  * Rows r >= n_e of the inputs may hold anything, those of dx are left
  * untouched; an expert without tokens has zero weight gradients.  fp32 sums, da
- * rounded once to bf16; the flags that choose GEMM kernels have no effect.  cfg->dtype SWITCH_BF16 only; workspace
- * switch_backward_workspace_size(). */
+ * rounded once to bf16; the flags that choose GEMM kernels have no effect.
+ * cfg->dtype SWITCH_BF16 only; workspace switch_backward_workspace_size(). */
 switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const void* xq,
                                               const void* x_scale, const void* hq,
                                               const void* h_scale, const int32_t* counts,

@@ -25,7 +25,7 @@
 //     from arrays of words [512 columns][slot] that the gather and the first
 //     product's drain write (a tile's rows are then consecutive);
 //   * warp 1 of the leader copies the scales to TMEM and issues the MMAs;
-//   * warps 4-11 drain: one feature a lane, 32 tokens at a time.  For the
+//   * warps 4-19 drain: one feature a lane, 32 tokens at a time.  For the
 //     hidden rows a token's scale is over the CTA's 128 features, that is 32
 //     lanes of four warps: a warp maximum per token, then one exchange through
 //     shared memory.

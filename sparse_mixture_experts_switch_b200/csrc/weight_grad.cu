@@ -8,7 +8,7 @@
 // bound by writing dw.  One persistent kernel on CTA pairs, 256 x 256 tiles; both
 // operands lie with m or n contiguous and are used as they lie (MN-major tiles,
 // 64 rows deep, one 4-D box of 64 rows x 2 x 64 columns per operand and CTA).
-//   * warps 0 and 2 load A and B through a ring of six stages, warp 1 of the
+//   * warps 0 and 2 load A and B through a ring of five stages, warp 1 of the
 //     leader issues (warp-uniform loops: expert_ffn_q8.cu says why);
 //   * 16 drain warps: 32 result rows x 64 columns each, in bf16 through a
 //     128-byte-swizzled box that one TMA store writes (it clips at the edges).
