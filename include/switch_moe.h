@@ -474,7 +474,9 @@ switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
  *   8-bit block rows in which a value above zero never becomes zero (it takes
  *   the smallest e4m3 value, 2^-9 times its scale), so hq > 0 is the ReLU's
  *   mask.
- * y is switch_expert_ffn's.  Rows r >= n_e of all outputs are left untouched.
+ * y is switch_expert_ffn's, bit for bit but where long sums of few tiles are taken
+ * in parts (the fp32 sums then have another order, fixed by the sizes).
+ * Rows r >= n_e of all outputs are left untouched.
  * x, slot_token and SWITCH_FLAG_ROWS_DISPATCHED as for switch_expert_ffn; the
  * flags that choose its GEMM kernels have no effect (the rows are always copied,
  * the products run on CTA pairs).  A token of a kept slot outside [0, T) sets

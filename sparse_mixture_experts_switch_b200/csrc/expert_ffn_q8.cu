@@ -83,6 +83,7 @@ struct Q8Params {
   uint8_t* hq;               // hidden: [N*C, n_out]
   uint8_t* hs;               // hidden: scale words [ceil(n_out / 512)][N*C], by bytes
   __nv_bfloat16* y;          // else: [N*C, n_out]
+  float* part;               // partial sums [parts][N*C][n_out], where there are parts
   DevErr* err;
   long long spin;
 };
@@ -133,7 +134,8 @@ __device__ __forceinline__ uint32_t acc_column(int acc, int nmma) {
 __device__ __forceinline__ void cp_async4_s(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-template <bool kHidden>
+// kParts: a tile's sum goes in parts (split_sum.cu).
+template <bool kHidden, bool kParts>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
     expert_gemm_q8_kernel(const __grid_constant__ RowMaps maps, Q8Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -186,7 +188,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
     fence_barrier_init();
   }
   __syncthreads();
-  const int total = pts[p.walk.N];
+  const int parts = kParts ? p.walk.parts : 1;
+  const int total = pts[p.walk.N] * parts;  // items
   if (cid >= total) {                       // same decision in both CTAs of the pair
     pdl_wait_prerequisites();
     return;
@@ -208,6 +211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
 
   RowWalk<kHidden> walk(p.walk, pts, kept);
   const int kstages = (kblocks + 1) / 2;
+  const int groups = (kblocks + 3) / 4;     // of scales: two stages each; parts are of whole groups
   if (warp == 0 || warp == 2) {
     // ------------------------------ TMA: warp 0 the weights, warp 2 the tokens
     const bool tokens = warp == 2;
@@ -215,8 +219,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     uint32_t issued_mask = 0, issued_phase = 0;
-    for (int tile = cid; tile < total; tile += ncl) {
+    for (int item = cid; item < total; item += ncl) {
       if (__any_sync(0xffffffffu, *abort_flag)) break;
+      const int tile = small_div(item, parts);
+      const StageRange range = part_stages(item - tile * parts, parts, groups);
+      const int ks1 = 2 * range.end < kstages ? 2 * range.end : kstages;
       const RowTile t = walk.at(tile);
       const int half = t.nmma >> 1;
       const int box = box_of(half);
@@ -227,7 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
       const uint32_t bytes = tokens ? box_rows(box) * kQK : kQWBytes;
       const uint32_t step = tokens ? kQTokBytes : kQWBytes;
       bool ok = true;
-      for (int ks = 0; ks < kstages; ++ks) {
+      for (int ks = 2 * range.begin; ks < ks1; ++ks) {
         if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, lim))) {
           if (lane == 0) {
             report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmProducer, tile);
@@ -273,12 +280,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
     // copies arrive on the group's barrier by themselves; the proxy fence between
     // them and tcgen05.cp is left to warps with no copies of their own in flight,
     // since it waits for all of a thread's.
-    const int groups = (kblocks + 3) / 4;
     const bool words = (p.kblk & 3) == 0;
-    int tile = cid, g = 0;
+    int item = cid, g = 0;
     RowTile t{};
+    StageRange range{};
     const uint8_t* wrow = nullptr;
     auto enter = [&]() {
+      const int tile = small_div(item, parts);
+      range = part_stages(item - tile * parts, parts, groups);
+      g = range.begin;
       t = walk.at(tile);
       int b = (t.f0 >> 7) + static_cast<int>(rank);
       if (b >= p.nblk_w) b = p.nblk_w - 1;             // features past the end: zero rows
@@ -287,11 +297,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
     int slot = 0;
     uint32_t phase = 0;
     enter();
-    while (tile < total) {
+    while (item < total) {
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       if (!__all_sync(0xffffffffu, mbar_wait(&sempty[slot], phase ^ 1u, lim))) {
         if (lane == 0) {
-          report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmProducer, tile);
+          report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmProducer, item);
           *abort_flag = 1;
         }
         break;
@@ -323,10 +333,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         if (lane == 0) mbar_arrive(&sfull[slot]);
       }
       if (++slot == kSfSlots) { slot = 0; phase ^= 1u; }
-      if (++g == groups) {
-        g = 0;
-        tile += ncl;
-        if (tile < total) enter();
+      if (++g == range.end) {
+        item += ncl;
+        if (item < total) enter();
       }
     }
     cp_async_wait_all();                               // none in flight behind this
@@ -341,8 +350,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
       int last_nmma = 0;
       bool any = false;
       const uint32_t smem0 = smem_u32(smem), sf0 = smem_u32(sf);
-      for (int tile = cid; tile < total; tile += ncl) {
+      for (int item = cid; item < total; item += ncl) {
         if (__any_sync(0xffffffffu, *abort_flag)) break;
+        const int tile = small_div(item, parts);
+        const StageRange range = part_stages(item - tile * parts, parts, groups);
+        const int ks0 = 2 * range.begin;
+        const int ks1 = 2 * range.end < kstages ? 2 * range.end : kstages;
         const int nmma = walk.at(tile).nmma;
         const uint32_t idesc = idesc_q8(256, nmma);
         bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, lim));
@@ -353,7 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         last_nmma = nmma;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc_column(acc, nmma);
-        for (int ks = 0; ok && ks < kstages; ++ks) {
+        for (int ks = ks0; ok && ks < ks1; ++ks) {
           if ((ks & 1) == 0) {                         // the scales of the next 4 K blocks
             ok = __all_sync(0xffffffffu, mbar_wait_cluster(&sfull[slot], sphase, lim));
             if (!ok) break;
@@ -381,7 +394,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
             // descriptors count 16 bytes: a 32-deep step is 2 of them
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_q8_pair(d_tmem, wd + 2 * k, td + 2 * k, id, sfa, sfa + 4, (ks | k) != 0 ? 1u : 0u);
+              umma_q8_pair(d_tmem, wd + 2 * k, td + 2 * k, id, sfa, sfa + 4,
+                           ks != ks0 || k != 0 ? 1u : 0u);
             if (2 * ks + 1 < kblocks) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
@@ -412,12 +426,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
       }
     } else {
       // -------------------------- follower: relay its scales to the leader
-      const int groups = (kblocks + 3) / 4;
       int slot = 0;
       uint32_t phase = 0;
-      for (int tile = cid; tile < total; tile += ncl) {
+      for (int item = cid; item < total; item += ncl) {
         bool ok = !__any_sync(0xffffffffu, *abort_flag);
-        for (int g = 0; ok && g < groups; ++g) {
+        const int tile = small_div(item, parts);
+        const StageRange range = part_stages(item - tile * parts, parts, groups);
+        for (int g = range.begin; ok && g < range.end; ++g) {
           ok = __all_sync(0xffffffffu, mbar_wait(&sfull[slot], phase, lim));
           if (!ok) {
             if (lane == 0) {
@@ -454,7 +469,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         else mbar_arrive_remote_relaxed(lead + 8u * b);
       }
     };
-    for (int tile = cid; tile < total; tile += ncl) {
+    for (int item = cid; item < total; item += ncl) {
+      const int tile = small_div(item, parts);
       bool ok = __all_sync(0xffffffffu, mbar_wait_sleepy(&tfull[acc], acc_phase, lim));
       if (kHidden) ok = all_of_barrier(ok, 1 + h);   // they meet below: go on together
       if (!ok) {
@@ -485,6 +501,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         }
         const int j0 = c * 32;
         const int jn = t.nv - j0 < 32 ? t.nv - j0 : 32;            // tokens of the chunk
+        if (kParts) {
+          // the part's sums, 32 features of a token a store; rows_join finishes them
+          if (on) {
+            float* dst = p.part + ((item - tile * parts) * p.slots + row0 + j0) * p.n_out + fb + lane;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < jn) dst[static_cast<int64_t>(j) * p.n_out] = __uint_as_float(v[j]);
+          }
+          continue;
+        }
         if (kHidden) {
           // the maximum as an upper bound with the same scale: the upper 16 bits of
           // the fp32 number, rounded up (a scale changes where the significand passes
@@ -580,8 +606,8 @@ bool map_weights(CUtensorMap* m, const void* base, int N, int n_out, int K) {
   const cuuint32_t b[3] = {kQK, 128, 1};
   return encode_u8(m, base, 3, dims, b, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-template <bool kHidden>
-cudaError_t run_q8(const void* rows, const void* weights, const Q8Params& p, int num_sms,
+template <bool kHidden, bool kParts>
+cudaError_t run_q8_parts(const void* rows, const void* weights, const Q8Params& p, int num_sms,
                    cudaStream_t st) {
   const int64_t slots = static_cast<int64_t>(p.walk.N) * p.walk.C;
   RowMaps maps;
@@ -592,10 +618,30 @@ cudaError_t run_q8(const void* rows, const void* weights, const Q8Params& p, int
   const size_t smem = kQSmem + sizeof(int) * (2 * p.walk.N + 2);
   static size_t smem_set[64] = {};
   cudaError_t e = ensure_smem_limit(
-      reinterpret_cast<const void*>(&expert_gemm_q8_kernel<kHidden>), smem, smem_set);
+      reinterpret_cast<const void*>(&expert_gemm_q8_kernel<kHidden, kParts>), smem, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_dependent(expert_gemm_q8_kernel<kHidden>, (num_sms / 2) * 2, kQThreads, smem, st, maps,
-                          p);
+  e = launch_dependent(expert_gemm_q8_kernel<kHidden, kParts>, (num_sms / 2) * 2, kQThreads, smem,
+                       st, maps, p);
+  if (e != cudaSuccess || !kParts) return e;
+  JoinArgs j{};
+  j.parts = p.walk.parts;
+  j.N = p.walk.N;
+  j.C = p.walk.C;
+  j.n_out = p.n_out;
+  j.counts = p.walk.counts;
+  j.part = p.part;
+  j.out = p.y;
+  j.hq = p.hq;
+  j.hs = p.hs;
+  j.num_sms = num_sms;
+  return launch_rows_join(kHidden ? kRowsHiddenQ8 : kRowsStore, j, st);
+}
+
+template <bool kHidden>
+cudaError_t run_q8(const void* rows, const void* weights, const Q8Params& p, int num_sms,
+                   cudaStream_t st) {
+  return p.walk.parts > 1 ? run_q8_parts<kHidden, true>(rows, weights, p, num_sms, st)
+                          : run_q8_parts<kHidden, false>(rows, weights, p, num_sms, st);
 }
 
 }  // namespace
@@ -618,6 +664,8 @@ cudaError_t launch_expert_ffn_q8(const FfnQ8Args& a, cudaStream_t st) {
   p.hs = reinterpret_cast<uint8_t*>(a.hw);
   p.err = a.err;
   p.spin = a.spin;
+  p.walk.parts = a.parts1;
+  p.part = a.part;
   cudaError_t e = run_q8<true>(a.xq, a.w1q, p, a.num_sms, st);
   if (e != cudaSuccess) return e;
   p.n_out = a.d;
@@ -625,6 +673,7 @@ cudaError_t launch_expert_ffn_q8(const FfnQ8Args& a, cudaStream_t st) {
   p.walk.ntiles_f = (a.d + 255) / 256;
   p.kblk = static_cast<int>(q8_blocks(a.F));
   p.nblk_w = static_cast<int>(q8_blocks(a.d));
+  p.walk.parts = a.parts2;
   p.as = a.hw;
   p.ws = a.w2s;
   p.hq = nullptr;

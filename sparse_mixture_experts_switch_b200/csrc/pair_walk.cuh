@@ -14,6 +14,7 @@ struct WalkParams {
   int ntiles_f;              // 256-feature tiles of an expert
   int64_t C;
   const int* counts;
+  int parts;                 // of the sum: items are tile * parts + part
 };
 
 __device__ __forceinline__ int kept_tokens(const WalkParams& p, int e) {
@@ -44,7 +45,7 @@ static __device__ void tiles_prefix_warp(const WalkParams& p, int npairs, int* p
       s128 += token_tiles(k, 7) * p.ntiles_f;
     }
   }
-  const int shift = __reduce_add_sync(0xffffffffu, s128) <= npairs ? 7 : 8;
+  const int shift = __reduce_add_sync(0xffffffffu, s128) * p.parts <= npairs ? 7 : 8;
   if (shift == 7) s = s128;
   if (lane == 0) kept[p.N] = shift;
   int inc = s;
@@ -74,6 +75,15 @@ struct RowTile {
 
 __device__ __forceinline__ int small_div(int a, int b) {      // b is 1 or 2 most of the time
   return b == 1 ? a : (b == 2 ? a >> 1 : a / b);
+}
+
+// Stages of one part of a sum of `stages`.
+struct StageRange {
+  int begin, end;
+};
+__device__ __forceinline__ StageRange part_stages(int part, int parts, int stages) {
+  if (parts == 1) return {0, stages};
+  return {part * stages / parts, (part + 1) * stages / parts};
 }
 
 // Tiles in the order of a pair's walk (tile numbers that only grow).  An

@@ -191,6 +191,8 @@ struct FfnQ8Args {
   uint8_t* hq;               // [N*C, F] scratch
   uint32_t* hw;              // scale words [ceil(F / 512)][N*C] scratch
   void* y;                   // [N*C, d] bf16
+  int parts1, parts2;        // of the products' sums (sum_parts)
+  float* part;               // scratch for them
   DevErr* err;
   long long spin;
   int num_sms;

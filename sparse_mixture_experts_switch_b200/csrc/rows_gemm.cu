@@ -47,6 +47,7 @@ struct RowsParams {
   uint8_t* hq;               // hidden: [N*C, n_out]
   uint8_t* hs;               //   [N*C, ceil(n_out / 128)]
   const uint32_t* mask;      // mask: [N*C, n_out / 32] bits
+  float* part;               // partial sums [parts][N*C][n_out], where there are parts
   DevErr* err;
   long long spin;
 };
@@ -57,7 +58,8 @@ __device__ __forceinline__ uint32_t relu_bf16x2(float lo, float hi) {
   return r;
 }
 
-template <int kMode, bool kWMN, bool kForward>
+// kParts: a tile's sum goes in parts (split_sum.cu).
+template <int kMode, bool kWMN, bool kForward, bool kParts>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
     rows_gemm_kernel(const __grid_constant__ RowMaps maps, RowsParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -100,7 +102,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
     fence_barrier_init();
   }
   __syncthreads();
-  const int total = pts[p.walk.N];
+  const int parts = kParts ? p.walk.parts : 1;
+  const int total = pts[p.walk.N] * parts;  // items
   if (cid >= total) {                       // same decision in both CTAs of the pair
     pdl_wait_prerequisites();
     return;
@@ -126,8 +129,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     uint32_t issued_mask = 0, issued_phase = 0;
-    for (int tile = cid; tile < total; tile += ncl) {
+    for (int item = cid; item < total; item += ncl) {
       if (__any_sync(0xffffffffu, *abort_flag)) break;
+      const int tile = small_div(item, parts);
+      const StageRange range = part_stages(item - tile * parts, parts, kstages);
       const RowTile t = walk.at(tile);
       const int half = t.nmma >> 1;
       const int box = box_of(half);
@@ -137,7 +142,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
                              : t.f0 + static_cast<int>(rank) * 128;
       const uint32_t bytes = tokens ? box_rows(box) * kRK * 2 : kRWBytes;
       bool ok = true;
-      for (int ks = 0; ks < kstages; ++ks) {
+      for (int ks = range.begin; ks < range.end; ++ks) {
         if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, lim))) {
           if (lane == 0) {
             report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmProducer, tile);
@@ -187,13 +192,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
       // a 16-deep step in descriptor units of 16 bytes: 32 bytes along a K-major
       // row, 16 rows of 128 bytes in an M-major tile
       constexpr uint32_t kWStep = kWMN ? 128u : 2u;
-      for (int tile = cid; tile < total; tile += ncl) {
+      for (int item = cid; item < total; item += ncl) {
         if (__any_sync(0xffffffffu, *abort_flag)) break;
+        const int tile = small_div(item, parts);
+        const StageRange range = part_stages(item - tile * parts, parts, kstages);
         const uint32_t idesc = idesc_bf16_f32_major(256, walk.at(tile).nmma, kWMN, false);
         bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, lim));
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kQTok);
-        for (int ks = 0; ok && ks < kstages; ++ks) {
+        for (int ks = range.begin; ok && ks < range.end; ++ks) {
           ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, lim));
           if (!ok) break;
           tc_fence_after();
@@ -203,7 +210,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_bf16_pair(d_tmem, wd + kWStep * k, td + 2 * k, idesc, (ks | k) != 0 ? 1u : 0u);
+              umma_bf16_pair(d_tmem, wd + kWStep * k, td + 2 * k, idesc,
+                             ks != range.begin || k != 0 ? 1u : 0u);
             if (2 * ks + 1 < kblocks) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
@@ -244,7 +252,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
     const int64_t nblk = q8_blocks(p.n_out);
     int acc = 0, par = 0;
     uint32_t acc_phase = 0;
-    for (int tile = cid; tile < total; tile += ncl) {
+    for (int item = cid; item < total; item += ncl) {
+      const int tile = small_div(item, parts);
       bool ok = __all_sync(0xffffffffu, mbar_wait_sleepy(&tfull[acc], acc_phase, lim));
       if (kMode == kRowsHidden) ok = all_of_barrier(ok, 1 + h);   // they meet below: go on together
       if (!ok) {
@@ -267,11 +276,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
         const int j0 = c * 32;
         const int jn = t.nv - j0 < 32 ? t.nv - j0 : 32;            // tokens of the chunk
         uint32_t bits = 0;
-        if (kMode == kRowsMask && on && lane < jn)
+        if (kMode == kRowsMask && !kParts && on && lane < jn)
           bits = __ldg(p.mask + (row0 + j0 + lane) * (p.n_out >> 5) + (fb >> 5));
         uint32_t v[32];
         tmem_ld32_issue(taddr + static_cast<uint32_t>(j0), v);
         tmem_ld_wait(v);
+        if (kParts) {
+          // the part's sums, 32 features of a token a store; rows_join finishes them
+          if (on) {
+            float* dst = p.part + ((item - tile * parts) * (p.walk.N * p.walk.C) + row0 + j0) *
+                                      p.n_out + fb + lane;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < jn) dst[static_cast<int64_t>(j) * p.n_out] = __uint_as_float(v[j]);
+          }
+          continue;
+        }
         if (kMode == kRowsMask) {
           bits = transpose_bits(bits, lane);
 #pragma unroll
@@ -348,8 +368,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
 }
 
-template <int kMode, bool kWMN, bool kForward>
-cudaError_t run_rows(const RowsGemmArgs& a, cudaStream_t st) {
+template <int kMode, bool kWMN, bool kForward, bool kParts>
+cudaError_t run_rows_parts(const RowsGemmArgs& a, cudaStream_t st) {
   const int64_t slots = static_cast<int64_t>(a.N) * a.C;
   RowMaps maps;
   bool ok = kWMN ? make_tmap_mn_major(&maps.w, a.w, a.n_out, a.K, a.N)
@@ -370,13 +390,35 @@ cudaError_t run_rows(const RowsGemmArgs& a, cudaStream_t st) {
   p.mask = a.mask;
   p.err = a.err;
   p.spin = a.spin;
+  p.walk.parts = a.parts;
+  p.part = a.part;
   const size_t smem = kRSmem + sizeof(int) * (2 * a.N + 2);
   static size_t smem_set[64] = {};
   cudaError_t e = ensure_smem_limit(
-      reinterpret_cast<const void*>(&rows_gemm_kernel<kMode, kWMN, kForward>), smem, smem_set);
+      reinterpret_cast<const void*>(&rows_gemm_kernel<kMode, kWMN, kForward, kParts>), smem, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_dependent(rows_gemm_kernel<kMode, kWMN, kForward>, (a.num_sms / 2) * 2, kRThreads,
-                          smem, st, maps, p);
+  e = launch_dependent(rows_gemm_kernel<kMode, kWMN, kForward, kParts>, (a.num_sms / 2) * 2,
+                       kRThreads, smem, st, maps, p);
+  if (e != cudaSuccess || !kParts) return e;
+  JoinArgs j{};
+  j.parts = a.parts;
+  j.N = a.N;
+  j.C = a.C;
+  j.n_out = a.n_out;
+  j.counts = a.counts;
+  j.part = a.part;
+  j.out = a.out;
+  j.hq = a.hq;
+  j.hs = a.hs;
+  j.mask = a.mask;
+  j.num_sms = a.num_sms;
+  return launch_rows_join(kMode, j, st);
+}
+
+template <int kMode, bool kWMN, bool kForward>
+cudaError_t run_rows(const RowsGemmArgs& a, cudaStream_t st) {
+  return a.parts > 1 ? run_rows_parts<kMode, kWMN, kForward, true>(a, st)
+                     : run_rows_parts<kMode, kWMN, kForward, false>(a, st);
 }
 
 }  // namespace

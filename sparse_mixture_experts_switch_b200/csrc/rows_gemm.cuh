@@ -2,12 +2,18 @@
 // over experts' rows (rows_gemm.cu), and of rows' transposes (weight_grad.cu).
 #pragma once
 
+#include <algorithm>
+#include <cmath>
+
 #include "backward.cuh"
 #include "q8.cuh"
 
 namespace smoe {
 
-enum RowsMode : int { kRowsHidden = 0, kRowsStore = 1, kRowsMask = 2 };
+enum RowsMode : int {
+  kRowsHidden = 0, kRowsStore = 1, kRowsMask = 2,
+  kRowsHiddenQ8 = 3,         // split_sum.cu: the hidden rows of the 8-bit FFN
+};
 
 constexpr float kQ8Least = 0.001953125f;               // 2^-9, the smallest e4m3 value
 // Limit of a failed kernel's last wait for copies in flight (about 20 ms; a load
@@ -36,6 +42,56 @@ __device__ __forceinline__ bool all_of_barrier(bool ok, int id) {
   return r != 0;
 }
 
+// Long sums with few tiles in parts (split_sum.cu says when and why).
+constexpr int kSplitPairs = 74;             // CTA pairs of a B200
+constexpr int kPartStages = 6;              // fewest stages of a part
+constexpr int64_t kSplitBytes = 24 << 20;   // most scratch
+// Parts of sums of `stages` stages: at most `most`, and so many that the stages
+// saved are worth the most against `bytes` of scratch a part, if they are worth it.
+inline int parts_of(int64_t stages, int64_t most, double bytes) {
+  most = std::min(most, stages / kPartStages);
+  if (most < 2) return 1;
+  constexpr double kStageUs = 0.28, kBytesPerUs = 2e6, kLaunchUs = 3;
+  const double best = std::sqrt(kStageUs * kBytesPerUs * static_cast<double>(stages) / bytes);
+  const int64_t s = best < 2 ? 2 : (best < static_cast<double>(most) ? static_cast<int64_t>(best) : most);
+  const double sd = static_cast<double>(s);
+  const double gain = kStageUs * static_cast<double>(stages) * (1 - 1 / sd) - sd * bytes / kBytesPerUs;
+  return gain > kLaunchUs ? static_cast<int>(s) : 1;
+}
+// A product over experts' rows: n_out results of the kept rows (A assignments at
+// most), `stages` stages of 128 bf16 or 256 codes each.
+inline int sum_parts(int64_t N, int64_t C, int64_t A, int64_t n_out, int64_t stages) {
+  if (A <= 0 || C <= 0) return 1;
+  const int64_t tiles = std::min(std::min(N, A) + A / 256, N * ((C + 255) / 256)) *
+                        ((n_out + 255) / 256);
+  return parts_of(stages, std::min(kSplitPairs / tiles, kSplitBytes / (4 * N * C * n_out)),
+                  4.0 * static_cast<double>(std::min(A, N * C)) * static_cast<double>(n_out));
+}
+// Most parts of the weight gradients' sums over an expert's rows, and those of an
+// expert with `stages` stages (64 rows each).
+inline int grad_parts(int64_t N, int64_t C, int64_t A, int64_t d, int64_t F) {
+  const int64_t tiles = 2 * N * ((d + 255) / 256) * ((F + 255) / 256);
+  if (tiles > kSplitPairs) return 1;
+  return parts_of((std::min(C, A / N) + 63) / 64, kSplitPairs / tiles,
+                  8.0 * static_cast<double>(N * d * F));
+}
+__host__ __device__ inline int grad_tile_parts(int stages, int most) {
+  const int s = stages / kPartStages;
+  return s < 1 ? 1 : (s < most ? s : most);
+}
+
+struct JoinArgs {
+  int parts, N, n_out;
+  int64_t C;
+  const int* counts;
+  const float* part;         // [parts][N*C][n_out]
+  void* out;                 // [N*C, n_out] bf16
+  uint8_t *hq, *hs;          // hidden: the rows in 8 bits
+  const uint32_t* mask;
+  int num_sms;
+};
+cudaError_t launch_rows_join(int mode, const JoinArgs& a, cudaStream_t st);
+
 struct RowsGemmArgs {
   int N, n_out, K;
   int64_t C;
@@ -45,6 +101,8 @@ struct RowsGemmArgs {
   void* out;                 // [N*C, n_out] bf16, kept rows only
   uint8_t *hq, *hs;          // hidden: the rows in 8 bits too
   const uint32_t* mask;      // da: bits [N*C, n_out / 32]
+  int parts;                 // of the sum (sum_parts; split_sum.cu)
+  float* part;               // scratch [parts][N*C][n_out] for more than one
   DevErr* err;
   long long spin;
   int num_sms;
@@ -64,11 +122,14 @@ struct WeightGradArgs {
   const int* counts;
   const void *a[2], *b[2];
   void* dw[2];
+  int parts;                 // most parts of a sum (grad_parts)
+  float* part;               // scratch [2][parts][N][M][Nn] for more than one
   DevErr* err;
   long long spin;
   int num_sms;
 };
 cudaError_t launch_weight_grads(const WeightGradArgs& a, cudaStream_t st);
+cudaError_t launch_grad_join(const WeightGradArgs& a, cudaStream_t st);
 
 // bf16 [outer][k][m] as MN-major operand tiles (rows_gemm.cu).
 bool make_tmap_mn_major(CUtensorMap* map, const void* base, int64_t m, int64_t k, int64_t outer);

@@ -48,7 +48,7 @@ struct Layout {
   // sums of dh, dropped-token list and its counter; top-2 and fp32 only:
   // the dX GEMM's fp32 rows per slot
   size_t probs_s, da, dgp, dh, dhp, dhs, wrp, dgate, rpart, colsum, drop_list, n_drop, dxs,
-      mask, bwd_total;
+      mask, part, bwd_total;
 };
 
 // Bytes 16..19 of the workspace: the loss kernel's completion ticket (kept
@@ -64,6 +64,32 @@ int ntiles_of(int64_t T) { return static_cast<int>((T + kTileTok - 1) / kTileTok
 // Routes per token: 2 with SWITCH_FLAG_TOP2, else 1.  Dispatch works on the
 // routes x T (token, expert) assignments, route-major.
 int routes_of(const switch_config_t& c) { return (c.flags & SWITCH_FLAG_TOP2) ? 2 : 1; }
+
+// Parts of the sums of the expert FFNs' products with 8-bit rows, and the bytes
+// of scratch they take.
+struct SplitPlan {
+  int q8_hidden, q8_out, hidden, out, da, dx, grads;
+  size_t fwd_bytes, bwd_bytes;
+};
+SplitPlan split_plan(const switch_config_t& c, int64_t C) {
+  SplitPlan s{1, 1, 1, 1, 1, 1, 1, 0, 0};
+  if (c.dtype != SWITCH_BF16) return s;
+  const int64_t A = routes_of(c) * c.T, N = c.n_experts, d = c.d_model, F = c.d_ff;
+  s.q8_hidden = sum_parts(N, C, A, F, (d + 255) / 256);
+  s.q8_out = sum_parts(N, C, A, d, (F + 255) / 256);
+  s.hidden = sum_parts(N, C, A, F, (d + 127) / 128);
+  s.out = sum_parts(N, C, A, d, (F + 127) / 128);
+  s.da = s.hidden;
+  s.dx = s.out;
+  s.grads = grad_parts(N, C, A, d, F);
+  auto bytes = [&](int64_t parts, int64_t values) {
+    return parts > 1 ? sizeof(float) * parts * values : size_t{0};
+  };
+  const size_t rows = std::max(bytes(s.hidden, N * C * F), bytes(s.out, N * C * d));
+  s.fwd_bytes = std::max(rows, std::max(bytes(s.q8_hidden, N * C * F), bytes(s.q8_out, N * C * d)));
+  s.bwd_bytes = std::max(rows, bytes(s.grads, 2 * N * d * F));
+  return s;
+}
 
 Layout layout_for(const switch_config_t& c, int64_t C) {
   const int64_t T = c.T;
@@ -98,7 +124,9 @@ Layout layout_for(const switch_config_t& c, int64_t C) {
   L.logits = take(sizeof(float) * N * T);
   L.xdisp = take(es * slots * static_cast<size_t>(c.d_model));
   L.hbuf = take(es * slots * static_cast<size_t>(c.d_ff));
-  L.ybuf = take(es * slots * static_cast<size_t>(c.d_model));
+  // (also the scratch of the expert FFNs' sums in parts)
+  const SplitPlan split = split_plan(c, C);
+  L.ybuf = take(std::max(es * slots * static_cast<size_t>(c.d_model), split.fwd_bytes));
   L.total = o;
   const int64_t ntn = (c.d_ff + 255) / 256;
   L.probs_s = take(sizeof(float) * N * T);      // router probabilities kept for the backward
@@ -120,6 +148,7 @@ Layout layout_for(const switch_config_t& c, int64_t C) {
                    : 0);
   // a bit per hidden value (the backward from 8-bit checkpoints)
   L.mask = take(c.dtype == SWITCH_BF16 ? slots * static_cast<size_t>(c.d_ff) / 8 : 0);
+  L.part = take(split.bwd_bytes);      // and of its backward's
   L.bwd_total = o;
   return L;
 }
@@ -1111,6 +1140,10 @@ switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
   a.err = c.err;
   a.spin = c.spin;
   a.num_sms = c.num_sms;
+  const SplitPlan split = split_plan(*cfg, c.C);
+  a.parts1 = split.q8_hidden;
+  a.parts2 = split.q8_out;
+  a.part = c.at<float>(c.L.ybuf);
   a.xq = static_cast<const uint8_t*>(xq);
   if (a.A <= kFewTokens) {
     a.xs = static_cast<const uint8_t*>(x_scale);
@@ -1158,7 +1191,10 @@ switch_status_t switch_expert_ffn_checkpoint(const switch_config_t* cfg, const v
                                 cfg->T, dispatched ? nullptr : c.ws + c.L.xdisp, false,
                                 static_cast<uint8_t*>(xq), static_cast<uint8_t*>(x_scale), c.err,
                                 c.st));
+  const SplitPlan split = split_plan(*cfg, c.C);
   RowsGemmArgs a = rows_args(cfg, c, counts);
+  a.part = c.at<float>(c.L.ybuf);
+  a.parts = split.hidden;
   a.n_out = cfg->d_ff;
   a.K = cfg->d_model;
   a.rows = rows;
@@ -1167,6 +1203,7 @@ switch_status_t switch_expert_ffn_checkpoint(const switch_config_t* cfg, const v
   a.hq = static_cast<uint8_t*>(hq);
   a.hs = static_cast<uint8_t*>(h_scale);
   SMOE_TRY(launch_rows_hidden(a, c.st));
+  a.parts = split.out;
   a.n_out = cfg->d_model;
   a.K = cfg->d_ff;
   a.rows = c.ws + c.L.hbuf;
@@ -1205,7 +1242,10 @@ switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const 
                               static_cast<const uint8_t*>(x_scale), xb, nullptr}};
   SMOE_TRY(launch_unpack_rows(S, counts, c.C, false, sets, 2, c.st));
   // da = (dy w2) where h > 0, dx = da w1, dw1 = da^T x, dw2 = dy^T h
+  const SplitPlan split = split_plan(*cfg, c.C);
   RowsGemmArgs a = rows_args(cfg, c, counts);
+  a.part = c.at<float>(c.L.part);
+  a.parts = split.da;
   a.n_out = F;
   a.K = d;
   a.rows = dy;
@@ -1213,6 +1253,7 @@ switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const 
   a.out = c.ws + c.L.da;
   a.mask = mask;
   SMOE_TRY(launch_rows_da(a, c.st));
+  a.parts = split.dx;
   a.n_out = d;
   a.K = F;
   a.rows = c.ws + c.L.da;
@@ -1236,6 +1277,8 @@ switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const 
   g.a[1] = dy;
   g.b[1] = hb;
   g.dw[1] = dw2;
+  g.parts = split.grads;
+  g.part = c.at<float>(c.L.part);
   return cuda_status(launch_weight_grads(g, c.st));
 }
 

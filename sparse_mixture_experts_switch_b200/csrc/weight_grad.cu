@@ -45,7 +45,9 @@ struct GradMaps {
 struct GradParams {
   int N;
   int M[2], Nn[2], tm[2], tn[2];   // tm, tn: 256-wide tiles
-  int total[2];                    // tiles of the first gradient, of both
+  int total[2];                    // items of the first gradient, of both
+  int parts;                       // items of a tile: most parts of its sum
+  float* part;                     // partial sums [2][parts][N][M][Nn]
   int64_t C;
   const int* counts;
   DevErr* err;
@@ -53,15 +55,24 @@ struct GradParams {
 };
 
 struct GradTile {
-  int g, e, m0, n0, kept, kblocks;
+  int g, e, m0, n0, kept;
+  int part, parts;     // of the sum; an item with part >= parts is none
+  int kb0, kb1;        // its stages
 };
 
-// Tile t: first the tiles of gradient 0, then those of gradient 1; an expert's m
+// Item t, part t % parts of tile t / parts.  Tiles: first the tiles of gradient 0, then those of gradient 1; an expert's m
 // tiles vary fastest, then its n tiles.
+template <bool kParts>
 __device__ __forceinline__ GradTile grad_tile(const GradParams& p, int t) {
   GradTile r;
   r.g = t < p.total[0] ? 0 : 1;
   if (r.g) t -= p.total[0];
+  r.part = 0;
+  if (kParts) {
+    const int tile = t / p.parts;
+    r.part = t - tile * p.parts;
+    t = tile;
+  }
   const int tm = r.g ? p.tm[1] : p.tm[0];
   const int per = tm * (r.g ? p.tn[1] : p.tn[0]);
   r.e = t / per;
@@ -71,10 +82,14 @@ __device__ __forceinline__ GradTile grad_tile(const GradParams& p, int t) {
   r.m0 = (local - n * tm) * 256;
   const int64_t c = __ldg(p.counts + r.e);
   r.kept = static_cast<int>(c < 0 ? 0 : (c < p.C ? c : p.C));
-  r.kblocks = (r.kept + kGK - 1) / kGK;
+  const int kblocks = (r.kept + kGK - 1) / kGK;
+  r.parts = kParts ? grad_tile_parts(kblocks, p.parts) : 1;
+  r.kb0 = kParts ? r.part * kblocks / r.parts : 0;
+  r.kb1 = kParts ? (r.part + 1) * kblocks / r.parts : kblocks;
   return r;
 }
 
+template <bool kParts>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     weight_grad_kernel(const __grid_constant__ GradMaps maps, GradParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -142,11 +157,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     uint32_t tail_now = 0;                  // phase of each tail barrier's next use
     for (int tile = cid; tile < total; tile += ncl) {
       if (__any_sync(0xffffffffu, *abort_flag)) break;
-      const GradTile t = grad_tile(p, tile);
+      const GradTile t = grad_tile<kParts>(p, tile);
+      if (kParts && t.part >= t.parts) continue;
       const CUtensorMap* map = map0 + t.g;
       const int x = (is_b ? t.n0 : t.m0) + static_cast<int>(rank) * 128;
       bool ok = true;
-      for (int kb = 0; kb < t.kblocks; ++kb) {
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
         if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, lim))) {
           if (lane == 0) {
             report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmProducer, tile);
@@ -182,10 +198,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       // first asks for it
       const int ahead = tile + kGAhead * ncl;
       if (ahead < total) {
-        const GradTile u = grad_tile(p, ahead);
-        if ((is_b ? u.m0 : u.n0) == 0 && elect_one()) {
+        const GradTile u = grad_tile<kParts>(p, ahead);
+        if (u.part < u.parts && (is_b ? u.m0 : u.n0) == 0 && elect_one()) {
           const int xu = ((is_b ? u.n0 : u.m0) + static_cast<int>(rank) * 128) >> 6;
-          for (int kb = 0; kb < u.kblocks; ++kb)
+          for (int kb = u.kb0; kb < u.kb1; ++kb)
             tma_prefetch_l2_4d(map0 + u.g, 0, kb * kGK, xu, u.e);
         }
       }
@@ -209,10 +225,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     uint32_t tail_now = 0;
     for (int tile = cid; tile < total; tile += ncl) {
       if (__any_sync(0xffffffffu, *abort_flag)) break;
-      const GradTile t = grad_tile(p, tile);
+      const GradTile t = grad_tile<kParts>(p, tile);
+      if (kParts && t.part >= t.parts) continue;
       const int rows = t.kept % kGK;
-      if (rows != 0) {
-        const int s = (stage + t.kblocks - 1) % kGStages;
+      if (rows != 0 && t.part == t.parts - 1) {        // the expert's last stage
+        const int s = (stage + t.kb1 - t.kb0 - 1) % kGStages;
         if (!__all_sync(0xffffffffu, mbar_wait(&tail[s], (tail_now >> s) & 1u, lim))) {
           if (lane == 0) {
             report_error(p.err, SWITCH_ERR_TIMEOUT, kWhereGemmProducer, tile);
@@ -236,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           else mbar_arrive_remote(full_lead + 8u * s);
         }
       }
-      stage = (stage + t.kblocks) % kGStages;
+      stage = (stage + t.kb1 - t.kb0) % kGStages;
     }
   } else if (warp == 1) {
     // ------------------------------------------------- MMA issuer (leader)
@@ -248,11 +265,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const uint32_t smem0 = smem_u32(smem);
       for (int tile = cid; tile < total; tile += ncl) {
         if (__any_sync(0xffffffffu, *abort_flag)) break;
-        const GradTile t = grad_tile(p, tile);
+        const GradTile t = grad_tile<kParts>(p, tile);
+        if (kParts && t.part >= t.parts) continue;
         bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, lim));
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
-        for (int kb = 0; ok && kb < t.kblocks; ++kb) {
+        for (int kb = t.kb0; ok && kb < t.kb1; ++kb) {
           ok = __all_sync(0xffffffffu, (kb + 1) * kGK > t.kept
                                            ? mbar_wait_cluster(&full[stage], phase, lim)
                                            : mbar_wait(&full[stage], phase, lim));
@@ -265,7 +283,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             // a 16-deep step: 16 rows of 128 bytes, in descriptor units of 16 bytes
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_bf16_pair(d_tmem, ad + 128 * k, bd + 128 * k, idesc, (kb | k) != 0 ? 1u : 0u);
+              umma_bf16_pair(d_tmem, ad + 128 * k, bd + 128 * k, idesc,
+                             kb != t.kb0 || k != 0 ? 1u : 0u);
             umma_commit_pair(&empty[stage], 0x3);
           }
           any = true;
@@ -299,6 +318,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = cid; tile < total; tile += ncl) {
+      const GradTile t = grad_tile<kParts>(p, tile);
+      if (kParts && t.part >= t.parts) continue;
       const bool ok = __all_sync(0xffffffffu, mbar_wait_sleepy(&tfull[acc], acc_phase, lim));
       if (!ok) {
         if (lane == 0) {
@@ -308,13 +329,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         break;
       }
       tc_fence_after();
-      const GradTile t = grad_tile(p, tile);
       const int m = t.m0 + static_cast<int>(rank) * 128 + q * 32;
       const int n = t.n0 + cg * 64;
       const bool on = m < p.M[t.g] && n < p.Nn[t.g];   // warp-uniform: the box begins inside dw
+      if (kParts) {
+        // the part's sums in fp32: 32 columns at a time through the box, four rows
+        // of 128 bytes a store; grad_join finishes them
+        const int64_t nn = p.Nn[t.g];
+        float* dst = p.part +
+                     ((static_cast<int64_t>(t.g * p.parts + t.part) * p.N + t.e) * p.M[t.g] + m) * nn + n;
+#pragma unroll
+        for (int b = 0; b < 64; b += 32) {
+          uint32_t v[32];
+          if (on && t.kb1 > t.kb0) {
+            tmem_ld32_issue(tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                static_cast<uint32_t>(acc * 256 + cg * 64 + b), v);
+            tmem_ld_wait(v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+          }
+          if (!on) continue;
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            st_shared_v4u(box + lane * 128 + ((static_cast<uint32_t>(k) ^ swz) << 4), v[4 * k],
+                          v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int row = 4 * k + (lane >> 3);
+            *reinterpret_cast<float4*>(dst + row * nn + b + 4 * (lane & 7)) =
+                ld_shared_v4(box + row * 128 + ((lane ^ row) & 7) * 16);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive_relaxed(&tempty[acc]);
+          else mbar_arrive_remote_relaxed(tempty_lead + 8u * acc);
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+        continue;
+      }
       uint32_t pk[32];
       if (on) {
-        if (t.kblocks > 0) {
+        if (t.kb1 > t.kb0) {
           uint32_t v[32], u[32];
           const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                  static_cast<uint32_t>(acc * 256 + cg * 64);
@@ -365,6 +426,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
 }
 
+template <bool kParts>
+cudaError_t run_grads(const GradMaps& maps, const GradParams& p, int num_sms, cudaStream_t st) {
+  static size_t smem_set[64] = {};
+  const cudaError_t e = ensure_smem_limit(
+      reinterpret_cast<const void*>(&weight_grad_kernel<kParts>), kGSmem, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(weight_grad_kernel<kParts>, (num_sms / 2) * 2, kGThreads, kGSmem, st, maps,
+                          p);
+}
+
 }  // namespace
 
 cudaError_t launch_weight_grads(const WeightGradArgs& a, cudaStream_t st) {
@@ -375,6 +446,8 @@ cudaError_t launch_weight_grads(const WeightGradArgs& a, cudaStream_t st) {
   p.counts = a.counts;
   p.err = a.err;
   p.spin = a.spin;
+  p.parts = a.parts;
+  p.part = a.part;
   int64_t total = 0;
   for (int g = 0; g < 2; ++g) {
     bool ok = make_tmap_mn_major(&maps.a[g], a.a[g], a.M[g], a.C, a.N);
@@ -385,15 +458,13 @@ cudaError_t launch_weight_grads(const WeightGradArgs& a, cudaStream_t st) {
     p.Nn[g] = a.Nn[g];
     p.tm[g] = (a.M[g] + 255) / 256;
     p.tn[g] = (a.Nn[g] + 255) / 256;
-    total += static_cast<int64_t>(a.N) * p.tm[g] * p.tn[g];
+    total += static_cast<int64_t>(a.N) * p.tm[g] * p.tn[g] * a.parts;
     if (total > INT32_MAX) return cudaErrorInvalidValue;
     p.total[g] = static_cast<int>(total);
   }
-  static size_t smem_set[64] = {};
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(&weight_grad_kernel), kGSmem,
-                                    smem_set);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(weight_grad_kernel, (a.num_sms / 2) * 2, kGThreads, kGSmem, st, maps, p);
+  if (a.parts == 1) return run_grads<false>(maps, p, a.num_sms, st);
+  const cudaError_t e = run_grads<true>(maps, p, a.num_sms, st);
+  return e != cudaSuccess ? e : launch_grad_join(a, st);
 }
 
 }  // namespace smoe

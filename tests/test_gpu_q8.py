@@ -304,6 +304,18 @@ def test_ffn_q8_many_experts(sm):
             check(y[e, :n], want, tol, f"expert {e}")
 
 
+# few tiles and long sums: the products go in parts (the second, the first, both, the second
+# over many experts' few rows with most experts empty)
+PARTS = [(300, 64, 4672, 1, 1.0), (300, 4672, 64, 1, 1.0), (20, 5632, 5696, 1, 1.0),
+         (30, 128, 6016, 60, 4.0), (70, 192, 9472, 3, 2.0)]
+
+
+@pytest.mark.parametrize("T,d,F,N,cf", PARTS)
+@pytest.mark.parametrize("dispatched", [False, True])
+def test_ffn_q8_in_parts(sm, T, d, F, N, cf, dispatched):
+    test_ffn_q8(sm, T, d, F, N, cf, dispatched)
+
+
 @pytest.mark.parametrize("T", [3, 400])
 def test_ffn_q8_top2(sm, T):
     """Both routes of a token in slots of their experts: capacity over 2 T assignments, the
@@ -381,11 +393,20 @@ def test_bad_slot_token_is_reported(sm, T):
 
 def test_ffn_q8_forced_timeout_reports_and_recovers(sm):
     """Rows so wide that a tile takes longer than the hardware's own suspended wait (20 us),
-    which no limit of the call cuts short."""
-    T, d, F, N = 32, 65536, 128, 1
-    C, counts, slot, kept, x, w1, w2 = ffn_inputs(T, d, F, N, 1.0, 21)
-    a = [dev(t) for t in (*ref.to_q8(x), slot, counts, *ref.as_q8(*ref.quantize_weights(w1)),
-                          *ref.as_q8(*ref.quantize_weights(w2)))]
+    which no limit of the call cuts short: a CTA's 128 weight rows are 4 MB, 68000 cycles at
+    62 bytes each; and so many tiles that no sum goes in parts."""
+    T, d, F, N = 32, 32768, 9728, 1
+    C, counts, slot, kept = 32, *ref.routing(T, N, 32, 21)
+
+    def codes(*shape):
+        return torch.randint(0, 120, shape, dtype=torch.uint8, device="cuda")
+
+    def scales(*shape):
+        return torch.full(shape, 110, dtype=torch.uint8, device="cuda")
+
+    torch.manual_seed(21)
+    a = (codes(T, d), scales(T, d // 128), dev(slot), dev(counts), codes(N, F, d),
+         scales(N, F // 128, d // 128), codes(N, d, F), scales(N, d // 128, F // 128))
 
     def run(spin):
         cfg = sm.config(T, d, F, N, 1.0, spin_limit=spin)
@@ -401,14 +422,18 @@ def test_ffn_q8_forced_timeout_reports_and_recovers(sm):
 
 def test_checkpoint_forced_timeouts_report_and_recover(sm):
     """The same for the products of the FFN with checkpoint and of its backward."""
-    T, d, F, N = 64, 65536, 128, 1
+    T, d, F, N = 64, 16384, 9728, 1
     C = sm.switch_capacity(T, N, 1.0)
-    g = gen(5)
+    g = torch.Generator("cuda").manual_seed(5)
     flags = sm.FLAG_ROWS_DISPATCHED
-    x = dev(torch.randn(C, d, generator=g).bfloat16())
-    dy = dev(torch.randn(N, C, d, generator=g).bfloat16())
-    w1 = dev((torch.randn(N, F, d, generator=g) * 0.01).bfloat16())
-    w2 = dev((torch.randn(N, d, F, generator=g) * 0.01).bfloat16())
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device="cuda", dtype=torch.bfloat16)
+
+    x = rand(C, d)
+    dy = rand(N, C, d)
+    w1 = 0.01 * rand(N, F, d)
+    w2 = 0.01 * rand(N, d, F)
     counts = torch.tensor([T - 3], dtype=torch.int32, device="cuda")
 
     def run(spin):
@@ -440,6 +465,21 @@ CKPT = [(1, 64, 64, 1, 1.0, ()), (300, 64, 128, 2, 1.0, ()), (700, 320, 832, 6, 
 @pytest.mark.parametrize("T,d,F,N,cf,dead", CKPT)
 @pytest.mark.parametrize("flags", [0, 32, 64, 128, 2048])
 def test_ffn_checkpoint(sm, T, d, F, N, cf, dead, flags):
+    check_ffn_checkpoint(sm, T, d, F, N, cf, dead, flags, True)
+
+
+# sums in parts: hidden and da; out and dx; all four; dw1 and dw2, with an expert without rows
+CKPT_PARTS = [(300, 2368, 64, 1, 1.0, ()), (300, 64, 4672, 1, 1.0, ()), (37, 2368, 2432, 1, 1.0, ()),
+              (2500, 64, 192, 1, 1.0, ()), (8000, 128, 192, 3, 2.0, (1,)), (90, 128, 9472, 3, 4.0, (0,))]
+
+
+@pytest.mark.parametrize("T,d,F,N,cf,dead", CKPT_PARTS)
+@pytest.mark.parametrize("flags", [0, 32])
+def test_ffn_checkpoint_in_parts(sm, T, d, F, N, cf, dead, flags):
+    check_ffn_checkpoint(sm, T, d, F, N, cf, dead, flags, False)
+
+
+def check_ffn_checkpoint(sm, T, d, F, N, cf, dead, flags, exact):
     C, counts, slot, kept, x, w1, w2 = ffn_inputs(T, d, F, N, cf, T + d + F + 1, dead)
     x, w1, w2 = x.bfloat16(), w1.bfloat16(), w2.bfloat16()
     cfg = sm.config(T, d, F, N, cf, flags=flags)
@@ -457,11 +497,11 @@ def test_ffn_checkpoint(sm, T, d, F, N, cf, dead, flags):
     sm.switch_expert_ffn_checkpoint(cfg, dev(src), dev(slot), dev(counts), dev(w1), dev(w2), y, xq,
                                     xs, hq, hs, ws)
     assert sm.switch_get_device_error(ws)[0] == 0
-    # the FFN itself is switch_expert_ffn's, bit for bit
+    # the FFN itself is switch_expert_ffn's, bit for bit unless sums go in parts
     y2 = torch.full_like(y, -7.0)
     ws2 = sm.workspace(cfg)
     sm.switch_expert_ffn(cfg, dev(src), dev(slot), dev(counts), dev(w1), dev(w2), y2, ws2)
-    assert torch.equal(y, y2)
+    assert torch.equal(y, y2) or not exact
     for e in range(N):
         n = int(kept[e])
         r = slice(e * C, e * C + n)
@@ -481,6 +521,13 @@ def test_ffn_checkpoint(sm, T, d, F, N, cf, dead, flags):
         # bf16's half step, then e4m3's (or its smallest value, taken for smaller ones)
         tol = 2.0 ** -8 * h + torch.maximum(2.0 ** -4 * (1 + 2.0 ** -8) * h, 2.0 ** -9 * s) + err
         check(got, h, tol, f"hidden rows of expert {e}")
+        # y: the hidden rows' fp32 errors and bf16 rounding, its own sum and rounding
+        b = w2[e].double()
+        want = h @ b.T
+        eh = err + 2.0 ** -8 * (h + err)
+        tol = eh @ b.abs().T + F * F32 * ((h + eh) @ b.abs().T)
+        check(y[e, :n], want, tol + 2.0 ** -8 * (want.abs() + tol), f"y of expert {e}")
+        assert (y[e, n:] == -7).all()
 
 
 @pytest.mark.parametrize("T,d,F,N,cf,dead", CKPT)
@@ -529,6 +576,11 @@ def test_ffn_backward_q8(sm, T, d, F, N, cf, dead, flags):
             # independent roundings: half a step of the result and of da, in norm
             off = (got.cpu().double() - want).norm() / want.norm()
             assert off <= 2.0 ** -7, (name, e, off)
+
+
+@pytest.mark.parametrize("T,d,F,N,cf,dead", CKPT_PARTS)
+def test_ffn_backward_q8_in_parts(sm, T, d, F, N, cf, dead):
+    test_ffn_backward_q8(sm, T, d, F, N, cf, dead, 0)
 
 
 def test_ffn_backward_q8_by_differences(sm):
