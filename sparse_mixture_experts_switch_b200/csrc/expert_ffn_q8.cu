@@ -452,14 +452,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
   } else if (warp >= 4) {
     // --------------------------------------------------------- drain warps
     // Quarter q of the CTA's 128 features (one a lane); the kQHalves warps of a
-    // quarter take the chunks of 32 tokens in turn, first those whose columns the
-    // next tile may need.
+    // quarter take the chunks of 32 tokens in turn (from another one on in each
+    // tile: tiles of one chunk then drain side by side), first those whose columns
+    // the next tile may need.
     const int q = warp & 3;
     const int h = (warp - 4) >> 2;
     float* isv = reinterpret_cast<float*>(stage_out) + (warp - 4) * 32;   // tokens' 2^-e
     float* redh = red + h * 256;                       // [parity][quarter][32]
     int acc = 0, par = 0;
     uint32_t acc_phase = 0;
+    int first = h;                                     // the warp's first chunk of a tile
     // relaxed: only TMEM loads, which have been waited for, are handed over (a
     // release would hold the warp until its rows' stores had reached memory)
     auto arrive_lead = [&](uint64_t* bar, uint32_t lead, int b) {
@@ -489,16 +491,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
       const int64_t row0 = static_cast<int64_t>(t.e) * p.walk.C + t.t0;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                              acc_column(acc, t.nmma);
-      if (h >= 2 || h >= nch) arrive_lead(tover, tover_lead, acc);   // none of those
-      for (int i = h; i < nch; i += kQHalves) {
+      if (first >= 2 || first >= nch) arrive_lead(tover, tover_lead, acc);   // none of those
+      if (first >= nch) {
+        tc_fence_before();
+        arrive_lead(tempty, tempty_lead, acc);
+      }
+      for (int i = first; i < nch; i += kQHalves) {
         const int c = acc == 0 ? nch - 1 - i : i;
         uint32_t v[32];
         tmem_ld32_issue(taddr + static_cast<uint32_t>(c * 32), v);
         tmem_ld_wait(v);
-        if (i < 2) {                                               // at most 64 columns overlap
-          tc_fence_before();
-          arrive_lead(tover, tover_lead, acc);
-        }
+        if (i < 2 || i + kQHalves >= nch) tc_fence_before();
+        if (i < 2) arrive_lead(tover, tover_lead, acc);            // at most 64 columns overlap
+        if (i + kQHalves >= nch) arrive_lead(tempty, tempty_lead, acc);   // the warp's last
         const int j0 = c * 32;
         const int jn = t.nv - j0 < 32 ? t.nv - j0 : 32;            // tokens of the chunk
         if (kParts) {
@@ -565,8 +570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
           }
         }
       }
-      tc_fence_before();
-      arrive_lead(tempty, tempty_lead, acc);
+      first = (first + 1) % kQHalves;
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }

@@ -244,7 +244,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
   } else if (warp >= 4) {
     // --------------------------------------------------------- drain warps
     // Quarter q of the CTA's 128 features (one a lane); the kRHalves warps of a
-    // quarter take the chunks of 32 tokens in turn.
+    // quarter take the chunks of 32 tokens in turn, from another one on in each
+    // tile (tiles of one chunk then drain side by side).
     const int q = warp & 3;
     const int h = (warp - 4) >> 2;
     float* isv = is_all + (warp - 4) * 32;             // hidden: tokens' 2^-e
@@ -252,6 +253,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
     const int64_t nblk = q8_blocks(p.n_out);
     int acc = 0, par = 0;
     uint32_t acc_phase = 0;
+    int first = h;                                     // the warp's first chunk of a tile
+    // The accumulator goes back once the warp's last chunk is in registers.  Relaxed:
+    // only TMEM loads, which have been waited for, are handed over (a release would
+    // hold the warp until its rows' stores had reached memory).
+    auto hand_back = [&](int b) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive_relaxed(&tempty[b]);
+        else mbar_arrive_remote_relaxed(tempty_lead + 8u * b);
+      }
+    };
     for (int item = cid; item < total; item += ncl) {
       const int tile = small_div(item, parts);
       bool ok = __all_sync(0xffffffffu, mbar_wait_sleepy(&tfull[acc], acc_phase, lim));
@@ -272,7 +285,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
       const int64_t row0 = static_cast<int64_t>(t.e) * p.walk.C + t.t0;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                              static_cast<uint32_t>(acc * kQTok);
-      for (int c = h; c < nch; c += kRHalves) {
+      if (first >= nch) hand_back(acc);
+      for (int c = first; c < nch; c += kRHalves) {
         const int j0 = c * 32;
         const int jn = t.nv - j0 < 32 ? t.nv - j0 : 32;            // tokens of the chunk
         uint32_t bits = 0;
@@ -281,6 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
         uint32_t v[32];
         tmem_ld32_issue(taddr + static_cast<uint32_t>(j0), v);
         tmem_ld_wait(v);
+        if (c + kRHalves >= nch) hand_back(acc);
         if (kParts) {
           // the part's sums, 32 features of a token a store; rows_join finishes them
           if (on) {
@@ -348,14 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
         if (q == 0 && lane < jn)
           p.hs[(row0 + j0 + lane) * nblk + (fc >> 7)] = static_cast<uint8_t>(q8_scale_byte(ex));
       }
-      // relaxed: only TMEM loads, which have been waited for, are handed over (a
-      // release would hold the warp until its rows' stores had reached memory)
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (leader) mbar_arrive_relaxed(&tempty[acc]);
-        else mbar_arrive_remote_relaxed(tempty_lead + 8u * acc);
-      }
+      first = (first + 1) % kRHalves;
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
