@@ -39,7 +39,7 @@
 // eight MMAs.
 //
 // Measured, each product alone: 25278 kept tokens, 128 experts of 1024 x 4096,
-// 141 us (weights 537 MB, hidden rows 107 MB) and 116 us (671 MB in all); 16
+// 126 us (weights 537 MB, hidden rows 107 MB) and 116 us (671 MB in all); 16
 // experts of 4096 x 10240 with 3148 tokens 141 and 152 us.  There the weights'
 // stream (103 us at the copy rate) and shared memory (operands in and out at 128
 // bytes a cycle: about 470 cycles for a block of 104 tokens a CTA, the MMAs 416)
@@ -61,16 +61,19 @@ constexpr uint32_t kQStageBytes = 2 * (kQWBytes + kQTokBytes);   // W, W, tokens
 constexpr int kQHalves = 4;                            // drain warps per lane quarter
 constexpr int kQDrainWarps = 4 * kQHalves;
 constexpr int kQThreads = 128 + 32 * kQDrainWarps;
-constexpr int kSfSlots = 6;                            // ring of scale groups (512 columns each)
+constexpr int kSfSlots = 4;                            // ring of scale groups (512 columns each)
 constexpr int kSfTmemSlots = 4;
 constexpr uint32_t kSfBytes = 3 * 512;                 // weight rows, tokens 0-127, 128-255
 constexpr uint32_t kSfTmem = 448;                      // TMEM columns 448 + 16 i, i < 4
-constexpr uint32_t kQStageOut = 128;                   // per drain warp: 32 tokens' 2^-e
-constexpr uint32_t kQRedBytes = kQHalves * 2 * 4 * 128;   // maxima: [half][parity][quarter][32]
+constexpr uint32_t kQStageOut = 128;                   // hidden, per four warps: 32 tokens' 2^-e
+constexpr uint32_t kQRedBytes = kQHalves * 4 * 128;    // hidden: maxima [half][quarter][32]
+constexpr uint32_t kQRowBytes = 32 * 128;              // hidden: 32 tokens x 128 codes of four warps
 constexpr uint32_t kQBarBytes = 512;
 constexpr uint32_t kQTmemCols = 512;
-constexpr uint32_t kQSmem = 1024 + kQStages * kQStageBytes + kQDrainWarps * kQStageOut +
-                            kSfSlots * kSfBytes + kQRedBytes + kQBarBytes;   // + pts, kept
+constexpr uint32_t kQSmem = 1024 + kQStages * kQStageBytes + kQHalves * kQStageOut +
+                            kSfSlots * kSfBytes + kQRedBytes + kQHalves * kQRowBytes +
+                            kQBarBytes;                // + pts, kept
+static_assert(kQSmem + 8 * (1024 + 1) <= 232448, "a CTA's shared memory");
 
 struct Q8Params {
   WalkParams walk;
@@ -142,9 +145,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint8_t* stage_out = smem + kQStages * kQStageBytes;
-  uint8_t* sf = stage_out + kQDrainWarps * kQStageOut;
+  uint8_t* sf = stage_out + kQHalves * kQStageOut;
   float* red = reinterpret_cast<float*>(sf + kSfSlots * kSfBytes);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sf + kSfSlots * kSfBytes + kQRedBytes);
+  uint8_t* rows_out = reinterpret_cast<uint8_t*>(red) + kQRedBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(rows_out + kQHalves * kQRowBytes);
   uint64_t* empty = full + kQStages;        // full: leader, both CTAs' bytes; empty: local
   uint64_t* sfull = empty + kQStages;       // scales in shared memory (leader: both CTAs')
   uint64_t* sempty = sfull + kSfSlots;      // local: copied to TMEM
@@ -155,7 +159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* pts = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + kQBarBytes);   // [N + 1]
-  int* kept = pts + p.walk.N + 1;                                                          // [N + 1]
+  int* kept = pts + p.walk.N + 1;                      // [N + 1]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -285,6 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
     RowTile t{};
     StageRange range{};
     const uint8_t* wrow = nullptr;
+    uint32_t wb[4] = {};
     auto enter = [&]() {
       const int tile = small_div(item, parts);
       range = part_stages(item - tile * parts, parts, groups);
@@ -294,9 +299,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
       if (b >= p.nblk_w) b = p.nblk_w - 1;             // features past the end: zero rows
       wrow = p.ws + (static_cast<int64_t>(t.e) * p.nblk_w + b) * p.kblk;
     };
+    // the weight rows' bytes where their word is not aligned, asked for a group
+    // ahead (past the row's end: its last one)
+    auto ask = [&]() {
+      if (words || item >= total) return;
+      const int left = p.kblk - 4 * g;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) wb[k] = __ldg(wrow + 4 * g + (k < left ? k : left - 1));
+    };
     int slot = 0;
     uint32_t phase = 0;
     enter();
+    ask();
     while (item < total) {
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       if (!__all_sync(0xffffffffu, mbar_wait(&sempty[slot], phase ^ 1u, lim))) {
@@ -314,8 +328,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         const int r = 32 * j + lane;
         cp_async4_s(dst + 512 + (j >> 2) * 512 + (j & 3) * 4, src + (r < t.nv ? r : 0));
       }
-      // the weight rows' word, four times a lane; by plain loads where it is not
-      // aligned (bytes past the row's end: its last one)
+      // the weight rows' word, four times a lane
       if (words) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) cp_async4_s(dst + j * 4, wrow + 4 * g);
@@ -323,11 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         if (lane == 0) mbar_arrive_relaxed(&sfull[slot]);
       } else {
         cp_async_mbar_arrive_noinc(&sfull[slot]);
-        const int b0 = 4 * g, left = p.kblk - b0;
-        uint32_t u = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          u |= static_cast<uint32_t>(__ldg(wrow + b0 + (k < left ? k : left - 1))) << (8 * k);
+        const uint32_t u = wb[0] | wb[1] << 8 | wb[2] << 16 | wb[3] << 24;
         st_shared_v4u(dst, u, u, u, u);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sfull[slot]);
@@ -337,6 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         item += ncl;
         if (item < total) enter();
       }
+      ask();
     }
     cp_async_wait_all();                               // none in flight behind this
   } else if (warp == 1) {
@@ -457,9 +467,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
     // the next tile may need.
     const int q = warp & 3;
     const int h = (warp - 4) >> 2;
-    float* isv = reinterpret_cast<float*>(stage_out) + (warp - 4) * 32;   // tokens' 2^-e
-    float* redh = red + h * 256;                       // [parity][quarter][32]
-    int acc = 0, par = 0;
+    float* isv = reinterpret_cast<float*>(stage_out) + h * 32;   // tokens' 2^-e
+    float* r = red + h * 128;                          // [quarter][32]
+    int acc = 0;
     uint32_t acc_phase = 0;
     int first = h;                                     // the warp's first chunk of a tile
     // relaxed: only TMEM loads, which have been waited for, are handed over (a
@@ -526,34 +536,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
           for (int i = 0; i < 16; ++i)
             m[i] = __vmaxs2(__byte_perm(v[2 * i] + 0xFFFFu, v[2 * i + 1] + 0xFFFFu, 0x7632), 0u);
           const float mine = __uint_as_float(warp_token_max(m, lane));
-          float* r = redh + par * 128;
-          par ^= 1;
           r[q * 32 + lane] = mine;
           named_bar_sync(1 + h, 128);
           const float a = fmaxf(fmaxf(r[lane], r[32 + lane]), fmaxf(r[64 + lane], r[96 + lane]));
           const int ex = q8_exponent(a);
-          if (!on) continue;                           // (no shared memory touched yet)
-          // the token's 2^-e to every lane
-          __syncwarp();                                // the last chunk's are read
+          // the token's 2^-e to every lane (the four warps write the same; what they
+          // share is written after this chunk's first barrier, read before its second
+          // or the next chunk's first)
           isv[lane] = q8_inv_scale(ex);
           __syncwarp();
-          float4 sc[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sc[k] = reinterpret_cast<const float4*>(isv)[k];
           // codes of tokens 4k .. 4k + 3 of this feature in a word; a transpose of
-          // four lanes' words makes it four features of token 4k + lane % 4, and a
-          // store writes 4 tokens x 32 bytes
+          // four lanes' words makes it four features of token 4k + lane % 4.  The four
+          // warps' codes meet in shared memory (16-byte pieces swizzled by the token, no
+          // two lanes of a store in one bank) as rows of 128 bytes, 4 tokens a store:
+          // with stores of 4 tokens x 32 bytes straight from the warps the first product
+          // at Large's shape took 141 us against 126.
+          const uint32_t rows = smem_u32(rows_out) + h * kQRowBytes;
+          if (on) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t w = relu_e4m3x4(
-                __uint_as_float(v[4 * k]) * sc[k].x, __uint_as_float(v[4 * k + 1]) * sc[k].y,
-                __uint_as_float(v[4 * k + 2]) * sc[k].z, __uint_as_float(v[4 * k + 3]) * sc[k].w);
-            const uint32_t z = transpose_bytes(w, lane);
-            const int rr = 4 * k + (lane & 3);
-            if (rr < jn)
-              *reinterpret_cast<uint32_t*>(p.hq + (row0 + j0 + rr) * p.n_out + fb + (lane & ~3)) = z;
+            for (int k = 0; k < 8; ++k) {
+              if (4 * k >= jn) break;
+              const float4 sc = reinterpret_cast<const float4*>(isv)[k];
+              const uint32_t w = relu_e4m3x4(
+                  __uint_as_float(v[4 * k]) * sc.x, __uint_as_float(v[4 * k + 1]) * sc.y,
+                  __uint_as_float(v[4 * k + 2]) * sc.z, __uint_as_float(v[4 * k + 3]) * sc.w);
+              const uint32_t z = transpose_bytes(w, lane);
+              const uint32_t piece = static_cast<uint32_t>(q * 2 + (lane >> 4)) ^ ((lane & 3u) << 1);
+              st_shared_u32(rows + (4 * k + (lane & 3)) * 128 + piece * 16 + (lane & 12), z);
+            }
           }
-          if (q == 0 && lane < jn)
+          named_bar_sync(1 + h, 128);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rr = 8 * q + 4 * i + (lane >> 3), c16 = lane & 7;
+            if (rr < jn && fc + c16 * 16 < p.n_out)
+              *reinterpret_cast<float4*>(p.hq + (row0 + j0 + rr) * p.n_out + fc + c16 * 16) =
+                  ld_shared_v4(rows + rr * 128 + ((c16 ^ ((rr & 3) << 1)) << 4));
+          }
+          if (q == 0 && on && lane < jn)
             p.hs[(static_cast<int64_t>(fc >> 9) * p.slots + row0 + j0 + lane) * 4 + ((fc >> 7) & 3)] =
                 static_cast<uint8_t>(q8_scale_byte(ex));
         } else if (on) {

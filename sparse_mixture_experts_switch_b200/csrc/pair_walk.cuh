@@ -18,7 +18,7 @@ struct WalkParams {
 };
 
 __device__ __forceinline__ int kept_tokens(const WalkParams& p, int e) {
-  const int64_t c = p.counts[e];
+  const int64_t c = __ldg(p.counts + e);
   return static_cast<int>(c < 0 ? 0 : (c < p.C ? c : p.C));
 }
 // Token tiles of an expert, of at most 2^shift tokens each.
@@ -26,8 +26,8 @@ __device__ __forceinline__ int token_tiles(int kept, int shift) {
   return (kept + (1 << shift) - 1) >> shift;
 }
 
-// Per expert: its kept tokens, and the exclusive prefix of its tiles (token
-// tiles x feature tiles); one warp.  The tiles take up to 256 tokens, or 128 where
+// Per expert its kept tokens, and the exclusive prefix of its tiles (token tiles x
+// feature tiles); one warp.  The tiles take up to 256 tokens, or 128 where
 // even then every pair has one tile at most: a tile of 128 tokens takes about 300
 // cycles for a block of the sum, one of 256 takes 512 (8-bit FFN of 300 tokens, one
 // expert of 2048 x 4096: 26.8 against 29.0 us; where it makes two rounds of tiles out
@@ -91,7 +91,9 @@ __device__ __forceinline__ StageRange part_stages(int part, int parts, int stage
 // weight tile.  A product that reads what the one before it wrote takes the list
 // from its end (kForward false): the last experts' rows, written last, are the
 // ones still in L2.  The walk
-// remembers its expert: a search per tile would cost more than a short tile.
+// remembers its expert and looks 32 on at a time, one a lane, so all of a warp's
+// lanes call it together (one lane going from expert to expert took 1000 cycles
+// where the tiles of 8 lie between a pair's next two).
 template <bool kForward>
 struct RowWalk {
   const WalkParams& p;
@@ -100,20 +102,15 @@ struct RowWalk {
   __device__ __forceinline__ RowWalk(const WalkParams& p_, const int* pts_, const int* kept_)
       : p(p_), pts(pts_), kept(kept_), e(kForward ? 0 : p_.N - 1) {}
   __device__ __forceinline__ RowTile at(int tile) {
+    const int lane = threadIdx.x & 31;
     if (!kForward) tile = pts[p.N] - 1 - tile;
-    int steps = 0;
-    while (kForward ? pts[e + 1] <= tile : pts[e] > tile) {
-      if (++steps > 8) {                     // far: halve the rest
-        int lo = kForward ? e : 0, hi = kForward ? p.N : e;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (pts[mid] <= tile) lo = mid; else hi = mid;
-        }
-        e = lo;
-        break;
-      }
-      e += kForward ? 1 : -1;
-    }
+    int n;
+    do {                                     // (the prefix never falls)
+      const int i = kForward ? e + 1 + lane : e - lane;
+      n = __popc(__ballot_sync(0xffffffffu, kForward ? i <= p.N && pts[i] <= tile
+                                                     : i >= 0 && pts[i] > tile));
+      e += kForward ? n : -n;
+    } while (n == 32);
     RowTile t;
     t.e = e;
     const int k = kept[e];

@@ -13,7 +13,7 @@
 // tile), up to 256 of an expert's tokens as its N, warp-uniform issue loops, two
 // loading warps, stages of eight MMAs (two blocks of 64 columns).  Measured,
 // each product alone, 25278 kept tokens, 128 experts of 1024 x 4096 (1.07 GB of
-// weights): hidden 243 us (1.4 GB with both forms of the rows), out 225 (1.3 GB),
+// weights): hidden 238 us (1.4 GB with both forms of the rows), out 225 (1.3 GB),
 // da 220, dx 213: 88 to 96% of the copy rate, bound by memory.  Two
 // accumulators of 256 columns fill the TMEM.  The weights are read as they lie:
 // [f][k] (K-major) in the forward, [k][f] (M-major) in the backward, where one
@@ -75,7 +75,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* pts = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);   // [N + 1]
-  int* kept = pts + p.walk.N + 1;                                              // [N + 1]
+  int* kept = pts + p.walk.N + 1;                      // [N + 1]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
