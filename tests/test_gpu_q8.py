@@ -769,6 +769,57 @@ def test_chain_on_a_side_stream_and_in_graphs(sm):
     assert torch.equal(got, a()) and not torch.equal(got, want_a)
 
 
+def test_parts_repeat_and_replay(sm):
+    """Sums in parts give the same bits each time: again, over scratch that holds NaN, on
+    another stream, and from a captured graph; one workspace serves all the calls."""
+    T, d, F, N, cf = 2600, 64, 4672, 1, 1.0
+    C = sm.switch_capacity(T, N, cf)
+    g = gen(77)
+    x = dev(torch.randn(C, d, generator=g).bfloat16())
+    dy = dev(torch.randn(N, C, d, generator=g).bfloat16())
+    w1 = dev((torch.randn(N, F, d, generator=g) * d ** -0.5).bfloat16())
+    w2 = dev((torch.randn(N, d, F, generator=g) * F ** -0.5).bfloat16())
+    counts = torch.tensor([300], dtype=torch.int32, device="cuda")
+    cfg = sm.config(T, d, F, N, cf, flags=sm.FLAG_ROWS_DISPATCHED)
+    ws = sm.backward_workspace(cfg)
+    (xq, xs), (hq, hs) = sm.q8_rows(C, d), sm.q8_rows(C, F)
+    (w1q, w1s), (w2q, w2s) = sm.q8_weights(N, F, d), sm.q8_weights(N, d, F)
+    sm.switch_quantize_weights(cfg, w1, w2, w1q, w1s, w2q, w2s)
+    out = [torch.zeros_like(t) for t in (dy, dy, dy, w1, w2)]
+
+    def run():
+        sm.switch_expert_ffn_checkpoint(cfg, x, None, counts, w1, w2, out[0], xq, xs, hq, hs, ws)
+        sm.switch_expert_ffn_q8(cfg, xq, xs, None, counts, w1q, w1s, w2q, w2s, out[1], ws)
+        sm.switch_expert_ffn_backward_q8(cfg, xq, xs, hq, hs, counts, w1, w2, dy, *out[2:], ws)
+
+    def same():
+        torch.cuda.synchronize()
+        ok = all(torch.equal(a, b) for a, b in zip(out, want))
+        for t in out:
+            t.zero_()
+        return ok
+
+    run()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in out]
+    assert all(torch.isfinite(t).all() and t.abs().max() > 0 for t in want)
+    ws[256:] = 255
+    run()
+    assert same()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    assert same()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        graph.replay()
+    assert same()
+    assert sm.switch_get_device_error(ws)[0] == 0
+
+
 def test_training_chain(sm):
     """Norm, FFN with 8-bit checkpoint, and both backward passes together: the gradients of
     sum(dy FFN(norm(x))) of a whole dispatched batch, against 64 bits."""
