@@ -170,11 +170,11 @@ __global__ void __launch_bounds__(RG * S * 32, 2) few_gemm_kernel(FewParams p) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             b[h] = rb >= 0 && k * 128 + h * 64 < p.K
-                       ? __ldg(reinterpret_cast<const uint4*>(xrow + k * 128 + h * 64))
+                       ? *reinterpret_cast<const uint4*>(xrow + k * 128 + h * 64)
                        : zero;
           const float sw = scale_of(__ldg(wsrow + k));
-          const float sa0 = r0 < 0 ? 1.f : scale_of(__ldg(s0 + k));     // (no token: a zero row)
-          const float sa1 = r1 < 0 ? 1.f : scale_of(__ldg(s1 + k));
+          const float sa0 = r0 < 0 ? 1.f : scale_of(s0[k]);     // (no token: a zero row)
+          const float sa1 = r1 < 0 ? 1.f : scale_of(s1[k]);
           float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {

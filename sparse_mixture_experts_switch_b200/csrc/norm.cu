@@ -432,8 +432,7 @@ __global__ void __launch_bounds__(kNormThreads) gain_columns_kernel(NormBwdArgs 
 // its 32 warps every 32nd part (eight loads in flight, added in order), and the
 // warps' sums meet in a fixed tree.
 __global__ void __launch_bounds__(1024) gain_reduce_kernel(int nparts, int d,
-                                                           const float* __restrict__ part,
-                                                           float* __restrict__ dgain) {
+                                                           const float* part, float* dgain) {
   __shared__ float s[32][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;
@@ -445,7 +444,7 @@ __global__ void __launch_bounds__(1024) gain_reduce_kernel(int nparts, int d,
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int q = p0 + 32 * i;
-        u[i] = q < nparts ? __ldg(part + static_cast<int64_t>(q) * d + c) : 0.f;
+        u[i] = q < nparts ? part[static_cast<int64_t>(q) * d + c] : 0.f;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) v += u[i];

@@ -92,7 +92,9 @@ __device__ __forceinline__ uint4 q8_decode8(uint2 q, uint32_t byte) {
 // may take its place while that one ends, and waits (pdl_wait_prerequisites,
 // before anything that depends on earlier kernels of the same call, and before
 // leaving) until it and all before it are complete.  Never the first kernel of
-// a call: what the caller ran before is then complete.
+// a call: what the caller ran before is then complete.  What an earlier kernel of the
+// call wrote is read by plain loads (or TMA), not through the read-only path, whose
+// loads the compiler may take to before the wait.
 template <class... P, class... A>
 inline cudaError_t launch_dependent(void (*kernel)(P...), int grid, int block, size_t smem,
                                     cudaStream_t st, A... args) {

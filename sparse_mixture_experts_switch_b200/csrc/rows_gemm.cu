@@ -291,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
         const int jn = t.nv - j0 < 32 ? t.nv - j0 : 32;            // tokens of the chunk
         uint32_t bits = 0;
         if (kMode == kRowsMask && !kParts && on && lane < jn)
-          bits = __ldg(p.mask + (row0 + j0 + lane) * (p.n_out >> 5) + (fb >> 5));
+          bits = p.mask[(row0 + j0 + lane) * (p.n_out >> 5) + (fb >> 5)];
         uint32_t v[32];
         tmem_ld32_issue(taddr + static_cast<uint32_t>(j0), v);
         tmem_ld_wait(v);

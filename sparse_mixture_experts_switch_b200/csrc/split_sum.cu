@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(JoinArgs p) {
       if (on) *out = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
     } else if (kMode == kRowsMask) {
       if (!on) continue;
-      const uint32_t w = __ldg(p.mask + r * (p.n_out >> 5) + (col >> 5)) >> (col & 31);
+      const uint32_t w = p.mask[r * (p.n_out >> 5) + (col >> 5)] >> (col & 31);
       *out = make_uint2(pack_bf16x2(w & 1u ? s.x : 0.f, w & 2u ? s.y : 0.f),
                         pack_bf16x2(w & 4u ? s.z : 0.f, w & 8u ? s.w : 0.f));
     } else {
