@@ -546,11 +546,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
           isv[lane] = q8_inv_scale(ex);
           __syncwarp();
           // codes of tokens 4k .. 4k + 3 of this feature in a word; a transpose of
-          // four lanes' words makes it four features of token 4k + lane % 4.  The four
-          // warps' codes meet in shared memory (16-byte pieces swizzled by the token, no
-          // two lanes of a store in one bank) as rows of 128 bytes, 4 tokens a store:
-          // with stores of 4 tokens x 32 bytes straight from the warps the first product
-          // at Large's shape took 141 us against 126.
+          // four lanes' words makes it four features of token 4k + lane % 4, and the
+          // four warps' words meet in shared memory as rows (with stores of 4 tokens x
+          // 32 bytes straight from the warps the first product at Large's shape took
+          // 141 us against 126)
           const uint32_t rows = smem_u32(rows_out) + h * kQRowBytes;
           if (on) {
 #pragma unroll
@@ -560,19 +559,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
               const uint32_t w = relu_e4m3x4(
                   __uint_as_float(v[4 * k]) * sc.x, __uint_as_float(v[4 * k + 1]) * sc.y,
                   __uint_as_float(v[4 * k + 2]) * sc.z, __uint_as_float(v[4 * k + 3]) * sc.w);
-              const uint32_t z = transpose_bytes(w, lane);
-              const uint32_t piece = static_cast<uint32_t>(q * 2 + (lane >> 4)) ^ ((lane & 3u) << 1);
-              st_shared_u32(rows + (4 * k + (lane & 3)) * 128 + piece * 16 + (lane & 12), z);
+              st_shared_u32(row_word(rows, 4 * k, q, lane), transpose_bytes(w, lane));
             }
           }
           named_bar_sync(1 + h, 128);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int rr = 8 * q + 4 * i + (lane >> 3), c16 = lane & 7;
-            if (rr < jn && fc + c16 * 16 < p.n_out)
-              *reinterpret_cast<float4*>(p.hq + (row0 + j0 + rr) * p.n_out + fc + c16 * 16) =
-                  ld_shared_v4(rows + rr * 128 + ((c16 ^ ((rr & 3) << 1)) << 4));
-          }
+          store_rows(rows, p.hq, row0 + j0, jn, fc, p.n_out, q, lane);
           if (q == 0 && on && lane < jn)
             p.hs[(static_cast<int64_t>(fc >> 9) * p.slots + row0 + j0 + lane) * 4 + ((fc >> 7) & 3)] =
                 static_cast<uint8_t>(q8_scale_byte(ex));

@@ -176,6 +176,25 @@ __device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int lane) {
   const uint32_t t2 = __shfl_xor_sync(0xffffffffu, x, 2);
   return (lane & 2) ? __byte_perm(t2, x, 0x7632) : __byte_perm(x, t2, 0x5410);
 }
+// Rows of 128 codes of 32 tokens in shared memory, 32 codes from each of four
+// warps, in 16-byte pieces swizzled by the token (no two lanes of a store meet in a
+// bank).  Where lane `lane` of warp q has four features of token tok + lane % 4 ...
+__device__ __forceinline__ uint32_t row_word(uint32_t rows, int tok, int q, int lane) {
+  const int piece = (q * 2 + (lane >> 4)) ^ ((lane & 3) << 1);
+  return rows + static_cast<uint32_t>((tok + (lane & 3)) * 128 + piece * 16 + (lane & 12));
+}
+// ... and the four warps' stores of the first jn of them to rows row0 .. of out
+// [.., cols], columns col .. col + 127 (those below cols): 4 rows x 128 bytes each.
+__device__ __forceinline__ void store_rows(uint32_t rows, uint8_t* out, int64_t row0, int jn,
+                                           int col, int cols, int q, int lane) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int rr = 8 * q + 4 * i + (lane >> 3), c = lane & 7;
+    if (rr < jn && col + c * 16 < cols)
+      *reinterpret_cast<float4*>(out + (row0 + rr) * cols + col + c * 16) =
+          ld_shared_v4(rows + static_cast<uint32_t>(rr * 128 + ((c ^ ((rr & 3) << 1)) << 4)));
+  }
+}
 // Tokens j and j + 1 of this feature (16 bits each) as two features of token
 // j + lane % 2.
 __device__ __forceinline__ uint32_t transpose_halves(uint32_t w, int lane) {

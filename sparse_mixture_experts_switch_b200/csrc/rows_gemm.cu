@@ -36,9 +36,12 @@ constexpr uint32_t kRStageBytes = 2 * (kRWBytes + kRTokBytes);   // W, W, tokens
 constexpr int kRHalves = 4;                            // drain warps per lane quarter
 constexpr int kRDrainWarps = 4 * kRHalves;
 constexpr int kRThreads = 128 + 32 * kRDrainWarps;
-constexpr uint32_t kRIsBytes = kRDrainWarps * 128;     // hidden: tokens' 2^-e per drain warp
-constexpr uint32_t kRRedBytes = kRHalves * 2 * 4 * 128;   // hidden: maxima [half][parity][quarter]
-constexpr uint32_t kRSmem = 1024 + kRStages * kRStageBytes + kRIsBytes + kRRedBytes + 256;
+constexpr uint32_t kRIsBytes = kRHalves * 128;         // hidden, per four warps: 32 tokens' 2^-e
+constexpr uint32_t kRRedBytes = kRHalves * 4 * 128;    // hidden: maxima [half][quarter][32]
+constexpr uint32_t kRRowBytes = 32 * 128;              // hidden: 32 tokens x 128 codes of four warps
+constexpr uint32_t kRSmem = 1024 + kRStages * kRStageBytes + kRIsBytes + kRRedBytes +
+                            kRHalves * kRRowBytes + 256;   // + pts, kept
+static_assert(kRSmem + 8 * (1024 + 1) <= 232448, "a CTA's shared memory");
 
 struct RowsParams {
   WalkParams walk;
@@ -67,7 +70,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   float* is_all = reinterpret_cast<float*>(smem + kRStages * kRStageBytes);
   float* red = is_all + kRIsBytes / 4;
-  uint64_t* full = reinterpret_cast<uint64_t*>(red + kRRedBytes / 4);
+  uint8_t* rows_out = reinterpret_cast<uint8_t*>(red) + kRRedBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(rows_out + kRHalves * kRRowBytes);
   uint64_t* empty = full + kRStages;        // full: leader, both CTAs' bytes; empty: local
   uint64_t* tfull = empty + kRStages;       // local: accumulator ready
   uint64_t* tempty = tfull + 2;             // leader: accumulator drained
@@ -248,10 +252,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
     // tile (tiles of one chunk then drain side by side).
     const int q = warp & 3;
     const int h = (warp - 4) >> 2;
-    float* isv = is_all + (warp - 4) * 32;             // hidden: tokens' 2^-e
-    float* redh = red + h * 256;                       // hidden: [parity][quarter][32]
+    float* isv = is_all + h * 32;                      // hidden: tokens' 2^-e
+    float* r = red + h * 128;                          // hidden: [quarter][32]
     const int64_t nblk = q8_blocks(p.n_out);
-    int acc = 0, par = 0;
+    int acc = 0;
     uint32_t acc_phase = 0;
     int first = h;                                     // the warp's first chunk of a tile
     // The accumulator goes back once the warp's last chunk is in registers.  Relaxed:
@@ -335,32 +339,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
         uint32_t m[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) m[i] = pk[i];
-        float* r = redh + par * 128;
-        par ^= 1;
         r[q * 32 + lane] = __uint_as_float(warp_token_max(m, lane));
         named_bar_sync(1 + h, 128);
         const float a = fmaxf(fmaxf(r[lane], r[32 + lane]), fmaxf(r[64 + lane], r[96 + lane]));
         const int ex = q8_exponent(a);
-        if (!on) continue;
-        __syncwarp();                                  // the last chunk's are read
+        // (what the four warps share is written after this chunk's first barrier, read
+        // before its second or the next chunk's first; expert_ffn_q8.cu has the rows' layout)
         isv[lane] = q8_inv_scale(ex);
         __syncwarp();
+        const uint32_t rows = smem_u32(rows_out) + h * kRRowBytes;
+        if (on) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float4 s = reinterpret_cast<const float4*>(isv)[k];
-          // what is above zero stays above zero
-          const float x0 = bf16_lo(pk[2 * k]), x1 = bf16_hi(pk[2 * k]);
-          const float x2 = bf16_lo(pk[2 * k + 1]), x3 = bf16_hi(pk[2 * k + 1]);
-          const uint32_t w = relu_e4m3x4(fmaxf(x0 * s.x, x0 > 0.f ? kQ8Least : 0.f),
-                                         fmaxf(x1 * s.y, x1 > 0.f ? kQ8Least : 0.f),
-                                         fmaxf(x2 * s.z, x2 > 0.f ? kQ8Least : 0.f),
-                                         fmaxf(x3 * s.w, x3 > 0.f ? kQ8Least : 0.f));
-          const uint32_t z = transpose_bytes(w, lane);
-          const int rr = 4 * k + (lane & 3);
-          if (rr < jn)
-            *reinterpret_cast<uint32_t*>(p.hq + (row0 + j0 + rr) * p.n_out + fb + (lane & ~3)) = z;
+          for (int k = 0; k < 8; ++k) {
+            if (4 * k >= jn) break;
+            const float4 s = reinterpret_cast<const float4*>(isv)[k];
+            // what is above zero stays above zero
+            const float x0 = bf16_lo(pk[2 * k]), x1 = bf16_hi(pk[2 * k]);
+            const float x2 = bf16_lo(pk[2 * k + 1]), x3 = bf16_hi(pk[2 * k + 1]);
+            const uint32_t w = relu_e4m3x4(fmaxf(x0 * s.x, x0 > 0.f ? kQ8Least : 0.f),
+                                           fmaxf(x1 * s.y, x1 > 0.f ? kQ8Least : 0.f),
+                                           fmaxf(x2 * s.z, x2 > 0.f ? kQ8Least : 0.f),
+                                           fmaxf(x3 * s.w, x3 > 0.f ? kQ8Least : 0.f));
+            st_shared_u32(row_word(rows, 4 * k, q, lane), transpose_bytes(w, lane));
+          }
         }
-        if (q == 0 && lane < jn)
+        named_bar_sync(1 + h, 128);
+        store_rows(rows, p.hq, row0 + j0, jn, fc, p.n_out, q, lane);
+        if (q == 0 && on && lane < jn)
           p.hs[(row0 + j0 + lane) * nblk + (fc >> 7)] = static_cast<uint8_t>(q8_scale_byte(ex));
       }
       first = (first + 1) % kRHalves;
