@@ -183,10 +183,13 @@ __global__ void __launch_bounds__(RG * S * 32, 2) few_gemm_kernel(FewParams p) {
             mma_e4m3(c, x.z, z.z, x.w, z.w, b[h].z, b[h].w);
           }
           if (k + kDepth * S < kb_n) load_w(k + kDepth * S, a[u]);
-          sum[0] = fmaf(c[0] * sw, sa0, sum[0]);
-          sum[1] = fmaf(c[1] * sw, sa1, sum[1]);
-          sum[2] = fmaf(c[2] * sw, sa0, sum[2]);
-          sum[3] = fmaf(c[3] * sw, sa1, sum[3]);
+          // the scales' product first: a power of two, where a block's sum (2^-18 to
+          // 2^25 in size) times one scale alone may leave fp32's range
+          const float f0 = sw * sa0, f1 = sw * sa1;
+          sum[0] = fmaf(c[0], f0, sum[0]);
+          sum[1] = fmaf(c[1], f1, sum[1]);
+          sum[2] = fmaf(c[2], f0, sum[2]);
+          sum[3] = fmaf(c[3], f1, sum[3]);
         }
       }
       // the next weights on their way before the sums meet: this expert's again
