@@ -368,7 +368,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         const int ks1 = 2 * range.end < kstages ? 2 * range.end : kstages;
         const int nmma = walk.at(tile).nmma;
         const uint32_t idesc = idesc_q8(256, nmma);
-        bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, lim));
+        // The accumulator's last tile is drained.  Its tover was arrived at before its
+        // tempty, but relaxed and on another barrier, so that is waited for too: the
+        // wait below for the next phase of the same barrier (one parity bit) is then
+        // never met by the phase before it.
+        bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, lim) &&
+                                              mbar_wait_cluster(&tover[acc], acc_phase ^ 1u, lim));
         // columns that the last tile has too: its drain takes those first
         if (ok && nmma + last_nmma > static_cast<int>(kSfTmem))
           ok = __all_sync(0xffffffffu,
