@@ -405,7 +405,8 @@ switch_status_t switch_ep_experts(const switch_config_t* cfg, const switch_ep_t*
  * one scale for each block of 128 x 128: [N, ceil(rows / 128),
  * ceil(cols / 128)].  The library makes a block's scale the smallest power of
  * two s >= 2^-100 with max |v| <= 448 s and rounds v / s once, to nearest,
- * ties to even; an all-zero block has s = 2^-100.  It reads any scale byte
+ * ties to even; an all-zero block has s = 2^-100.  A NaN takes the code NaN and
+ * does not count for its block's scale.  It reads any scale byte
  * from 1 to 254 (products of scales beyond fp32's range overflow as fp32
  * does); 255 (NaN) is unspecified. */
 

@@ -534,12 +534,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         if (kHidden) {
           // the maximum as an upper bound with the same scale: the upper 16 bits of
           // the fp32 number, rounded up (a scale changes where the significand passes
-          // 1.75, a border that 16 bits hold; numbers above zero order as their bits,
-          // those below become 0, the ReLU)
+          // 1.75, a border that 16 bits hold; what is below zero becomes 0, the ReLU,
+          // and so does NaN, which does not count)
           uint32_t m[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            m[i] = __vmaxs2(__byte_perm(v[2 * i] + 0xFFFFu, v[2 * i + 1] + 0xFFFFu, 0x7632), 0u);
+            m[i] = max_bf16x2(__byte_perm(v[2 * i] + 0xFFFFu, v[2 * i + 1] + 0xFFFFu, 0x7632), 0u);
           const float mine = __uint_as_float(warp_token_max(m, lane));
           r[q * 32 + lane] = mine;
           named_bar_sync(1 + h, 128);

@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(RG * S * 32, 2) few_gemm_kernel(FewParams p) {
             float x = 0.f;
 #pragma unroll
             for (int j = 0; j < S; ++j) x += red[j][tok][4 * lane + i];
-            v[i] = on ? fmaxf(x, 0.f) : 0.f;
-            m = fmaxf(m, v[i]);
+            v[i] = on && !(x <= 0.f) ? x : 0.f;  // ReLU; NaN stays NaN
+            m = fmaxf(m, v[i]);                  // (and does not count)
           }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));

@@ -140,7 +140,7 @@ __device__ __forceinline__ int box_of(int half) {
   return half <= 8 ? 0 : (half <= 16 ? 1 : (half <= 32 ? 2 : (half <= 64 ? 3 : (half - 1) >> 4)));
 }
 
-// relu of four fp32 values as e4m3 codes, `a` in the lowest byte.
+// relu of four fp32 values as e4m3 codes (NaN stays NaN), `a` in the lowest byte.
 __device__ __forceinline__ uint32_t relu_e4m3x4(float a, float b, float c, float d) {
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
@@ -148,8 +148,21 @@ __device__ __forceinline__ uint32_t relu_e4m3x4(float a, float b, float c, float
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
+// The larger of two bf16 numbers, twice; of a number and NaN the number.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The larger of two numbers; NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Lane j: the maximum over the warp of token j, from 16 registers of two tokens
-// each (token 2 i in the low half of m[i]) compared as signed 16-bit numbers; the
+// each (token 2 i in the low half of m[i]), all bf16 numbers (NaN only where all are); the
 // result in the upper half.  Five exchanges halve the tokens that a lane still
 // follows: 16 shuffles (a warp reduction per token, 32 of two cycles of the whole
 // SM each, took 310-940 cycles of a chunk's drain).
@@ -161,10 +174,10 @@ __device__ __forceinline__ uint32_t warp_token_max(uint32_t (&m)[16], int lane) 
     for (int i = 0; i < n; ++i) {
       const uint32_t keep = up ? m[i + n] : m[i];
       const uint32_t send = up ? m[i] : m[i + n];
-      m[i] = __vmaxs2(keep, __shfl_xor_sync(0xffffffffu, send, 2 * n));
+      m[i] = max_bf16x2(keep, __shfl_xor_sync(0xffffffffu, send, 2 * n));
     }
   }
-  const uint32_t p = __vmaxs2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+  const uint32_t p = max_bf16x2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
   return (lane & 1) ? p & 0xFFFF0000u : p << 16;
 }
 

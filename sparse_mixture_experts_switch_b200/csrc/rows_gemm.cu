@@ -334,15 +334,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
           }
         }
         if (kMode != kRowsHidden) continue;
-        // 8 bits: the token's maximum over the CTA's 128 features (bf16 numbers
-        // that are not negative order as their bits)
+        // 8 bits: the token's maximum over the CTA's 128 features (without those that
+        // are NaN; zero where all are)
         uint32_t m[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) m[i] = pk[i];
         r[q * 32 + lane] = __uint_as_float(warp_token_max(m, lane));
         named_bar_sync(1 + h, 128);
         const float a = fmaxf(fmaxf(r[lane], r[32 + lane]), fmaxf(r[64 + lane], r[96 + lane]));
-        const int ex = q8_exponent(a);
+        const int ex = q8_exponent(fmaxf(a, 0.f));
         // (what the four warps share is written after this chunk's first barrier, read
         // before its second or the next chunk's first; expert_ffn_q8.cu has the rows' layout)
         isv[lane] = q8_inv_scale(ex);
@@ -353,13 +353,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRThreads, 1)
           for (int k = 0; k < 8; ++k) {
             if (4 * k >= jn) break;
             const float4 s = reinterpret_cast<const float4*>(isv)[k];
-            // what is above zero stays above zero
+            // what is above zero stays above zero, NaN stays NaN
             const float x0 = bf16_lo(pk[2 * k]), x1 = bf16_hi(pk[2 * k]);
             const float x2 = bf16_lo(pk[2 * k + 1]), x3 = bf16_hi(pk[2 * k + 1]);
-            const uint32_t w = relu_e4m3x4(fmaxf(x0 * s.x, x0 > 0.f ? kQ8Least : 0.f),
-                                           fmaxf(x1 * s.y, x1 > 0.f ? kQ8Least : 0.f),
-                                           fmaxf(x2 * s.z, x2 > 0.f ? kQ8Least : 0.f),
-                                           fmaxf(x3 * s.w, x3 > 0.f ? kQ8Least : 0.f));
+            const uint32_t w = relu_e4m3x4(max_nan(x0 * s.x, x0 > 0.f ? kQ8Least : 0.f),
+                                           max_nan(x1 * s.y, x1 > 0.f ? kQ8Least : 0.f),
+                                           max_nan(x2 * s.z, x2 > 0.f ? kQ8Least : 0.f),
+                                           max_nan(x3 * s.w, x3 > 0.f ? kQ8Least : 0.f));
             st_shared_u32(row_word(rows, 4 * k, q, lane), transpose_bytes(w, lane));
           }
         }

@@ -31,10 +31,8 @@ __device__ __forceinline__ uint32_t relu_pack(float lo, float hi) {
   asm("cvt.rn.relu.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// What a ReLU leaves orders as its bits; NaN above all.
-__device__ __forceinline__ int relu_bits(float v) {
-  return v != v ? 0x7FFFFFFF : max(__float_as_int(v), 0);
-}
+// What a ReLU leaves orders as its bits; NaN does not count.
+__device__ __forceinline__ int relu_bits(float v) { return max(__float_as_int(fmaxf(v, 0.f)), 0); }
 
 // Kept rows, a warp for each 128 columns of one, four a lane.
 template <int kMode>
