@@ -133,7 +133,13 @@ typedef struct {
 int64_t switch_capacity(int64_t T, int32_t n_experts, double capacity_factor);
 
 /* Bytes of device workspace every entry point below accepts for `cfg`
- * (the maximum over them).  Writes *bytes; validates cfg. */
+ * (the maximum over them).  Writes *bytes; validates cfg.  At sizes where long
+ * sums of few tiles go in parts (the FFNs on 8-bit rows; d_model or d_ff in the
+ * thousands and few rows) up to 24 MB of it is room for the parts, likewise in
+ * switch_backward_workspace_size().  Calls need only the rest: in a smaller
+ * workspace these sums go in fewer parts, or whole (their fp32 sums then have another
+ * order).  Where d_ff > 16 d_model, the backward's size also counts a bit per hidden
+ * value, which switch_expert_ffn_backward_q8 alone needs. */
 switch_status_t switch_workspace_size(const switch_config_t* cfg, size_t* bytes);
 
 /* Router [P1 "Switch Routing", gate equation; top-1; fp32 routing math].
@@ -476,7 +482,8 @@ switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
  *   the smallest e4m3 value, 2^-9 times its scale), so hq > 0 is the ReLU's
  *   mask.
  * y is switch_expert_ffn's, bit for bit but where long sums of few tiles are taken
- * in parts (the fp32 sums then have another order, fixed by the sizes).
+ * in parts (the fp32 sums then have another order, fixed by the sizes, the
+ * workspace's among them).
  * Rows r >= n_e of all outputs are left untouched.
  * x, slot_token and SWITCH_FLAG_ROWS_DISPATCHED as for switch_expert_ffn; the
  * flags that choose its GEMM kernels have no effect (the rows are always copied,

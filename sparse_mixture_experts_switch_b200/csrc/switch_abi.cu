@@ -48,7 +48,7 @@ struct Layout {
   // sums of dh, dropped-token list and its counter; top-2 and fp32 only:
   // the dX GEMM's fp32 rows per slot
   size_t probs_s, da, dgp, dh, dhp, dhs, wrp, dgate, rpart, colsum, drop_list, n_drop, dxs,
-      mask, part, bwd_total;
+      bwd_total;
 };
 
 // Bytes 16..19 of the workspace: the loss kernel's completion ticket (kept
@@ -66,28 +66,29 @@ int ntiles_of(int64_t T) { return static_cast<int>((T + kTileTok - 1) / kTileTok
 int routes_of(const switch_config_t& c) { return (c.flags & SWITCH_FLAG_TOP2) ? 2 : 1; }
 
 // Parts of the sums of the expert FFNs' products with 8-bit rows, and the bytes
-// of scratch they take.
+// of scratch they take: at most `fwd_room` and `bwd_room`.
 struct SplitPlan {
   int q8_hidden, q8_out, hidden, out, da, dx, grads;
   size_t fwd_bytes, bwd_bytes;
 };
-SplitPlan split_plan(const switch_config_t& c, int64_t C) {
+SplitPlan split_plan(const switch_config_t& c, int64_t C, size_t fwd_room, size_t bwd_room) {
   SplitPlan s{1, 1, 1, 1, 1, 1, 1, 0, 0};
   if (c.dtype != SWITCH_BF16) return s;
   const int64_t A = routes_of(c) * c.T, N = c.n_experts, d = c.d_model, F = c.d_ff;
-  s.q8_hidden = sum_parts(N, C, A, F, (d + 255) / 256);
-  s.q8_out = sum_parts(N, C, A, d, (F + 255) / 256);
-  s.hidden = sum_parts(N, C, A, F, (d + 127) / 128);
-  s.out = sum_parts(N, C, A, d, (F + 127) / 128);
-  s.da = s.hidden;
-  s.dx = s.out;
-  s.grads = grad_parts(N, C, A, d, F);
+  s.q8_hidden = sum_parts(N, C, A, F, (d + 255) / 256, fwd_room);
+  s.q8_out = sum_parts(N, C, A, d, (F + 255) / 256, fwd_room);
+  s.hidden = sum_parts(N, C, A, F, (d + 127) / 128, fwd_room);
+  s.out = sum_parts(N, C, A, d, (F + 127) / 128, fwd_room);
+  s.da = sum_parts(N, C, A, F, (d + 127) / 128, bwd_room);
+  s.dx = sum_parts(N, C, A, d, (F + 127) / 128, bwd_room);
+  s.grads = grad_parts(N, C, A, d, F, bwd_room);
   auto bytes = [&](int64_t parts, int64_t values) {
     return parts > 1 ? sizeof(float) * parts * values : size_t{0};
   };
-  const size_t rows = std::max(bytes(s.hidden, N * C * F), bytes(s.out, N * C * d));
-  s.fwd_bytes = std::max(rows, std::max(bytes(s.q8_hidden, N * C * F), bytes(s.q8_out, N * C * d)));
-  s.bwd_bytes = std::max(rows, bytes(s.grads, 2 * N * d * F));
+  s.fwd_bytes = std::max({bytes(s.q8_hidden, N * C * F), bytes(s.q8_out, N * C * d),
+                          bytes(s.hidden, N * C * F), bytes(s.out, N * C * d)});
+  s.bwd_bytes = std::max({bytes(s.da, N * C * F), bytes(s.dx, N * C * d),
+                          bytes(s.grads, 2 * N * d * F)});
   return s;
 }
 
@@ -124,9 +125,7 @@ Layout layout_for(const switch_config_t& c, int64_t C) {
   L.logits = take(sizeof(float) * N * T);
   L.xdisp = take(es * slots * static_cast<size_t>(c.d_model));
   L.hbuf = take(es * slots * static_cast<size_t>(c.d_ff));
-  // (also the scratch of the expert FFNs' sums in parts)
-  const SplitPlan split = split_plan(c, C);
-  L.ybuf = take(std::max(es * slots * static_cast<size_t>(c.d_model), split.fwd_bytes));
+  L.ybuf = take(es * slots * static_cast<size_t>(c.d_model));
   L.total = o;
   const int64_t ntn = (c.d_ff + 255) / 256;
   L.probs_s = take(sizeof(float) * N * T);      // router probabilities kept for the backward
@@ -146,11 +145,32 @@ Layout layout_for(const switch_config_t& c, int64_t C) {
   L.dxs = take(routes_of(c) == 2 || c.dtype != SWITCH_BF16
                    ? sizeof(float) * slots * static_cast<size_t>(c.d_model)
                    : 0);
-  // a bit per hidden value (the backward from 8-bit checkpoints)
-  L.mask = take(c.dtype == SWITCH_BF16 ? slots * static_cast<size_t>(c.d_ff) / 8 : 0);
-  L.part = take(split.bwd_bytes);      // and of its backward's
   L.bwd_total = o;
   return L;
+}
+
+// The calls on 8-bit rows take what they need beside the rows from regions that
+// they leave idle, so that the layer's own calls need no byte more for them:
+//   * forward: sums in parts from ybuf on, to the workspace's end;
+//   * backward: the hidden values' mask (a bit each) in ybuf, which holds it up to
+//     d_ff = 16 d_model, else from dgp on; behind it, to the end, sums in parts.
+// A workspace need only hold the layout (and that rare mask): what goes in parts
+// goes by the room there is, and the size functions add what the full number takes.
+size_t mask_tail(const switch_config_t& c, int64_t C) {
+  return c.d_ff > 16 * static_cast<int64_t>(c.d_model)
+             ? align_up(static_cast<size_t>(c.n_experts * C) * c.d_ff / 8, kAlign)
+             : 0;
+}
+size_t bwd_q8_scratch(const switch_config_t& c, int64_t C, const Layout& L) {
+  return L.dgp + mask_tail(c, C);
+}
+size_t workspace_bytes(const switch_config_t& c, int64_t C, bool backward) {
+  const Layout L = layout_for(c, C);
+  const SplitPlan s = split_plan(c, C, kSplitBytes, kSplitBytes);
+  const size_t fwd = std::max(L.total, L.ybuf + s.fwd_bytes);
+  if (!backward) return fwd;
+  return std::max({L.bwd_total, fwd,
+                   c.dtype == SWITCH_BF16 ? bwd_q8_scratch(c, C, L) + s.bwd_bytes : size_t{0}});
 }
 
 switch_status_t validate(const switch_config_t* c, int64_t* C_out) {
@@ -361,7 +381,7 @@ switch_status_t switch_workspace_size(const switch_config_t* cfg, size_t* bytes)
   switch_status_t s = validate(cfg, &C);
   if (s != SWITCH_OK) return s;
   if (bytes == nullptr) return SWITCH_ERR_INVALID_ARG;
-  *bytes = layout_for(*cfg, C).total;
+  *bytes = workspace_bytes(*cfg, C, false);
   return SWITCH_OK;
 }
 
@@ -370,7 +390,7 @@ switch_status_t switch_backward_workspace_size(const switch_config_t* cfg, size_
   switch_status_t s = validate(cfg, &C);
   if (s != SWITCH_OK) return s;
   if (bytes == nullptr) return SWITCH_ERR_INVALID_ARG;
-  *bytes = layout_for(*cfg, C).bwd_total;
+  *bytes = workspace_bytes(*cfg, C, true);
   return SWITCH_OK;
 }
 
@@ -1071,7 +1091,7 @@ static switch_status_t validate_q8(const switch_config_t* cfg, int64_t* C = null
   if (s != SWITCH_OK) return s;
   return cfg->dtype == SWITCH_BF16 ? SWITCH_OK : SWITCH_ERR_UNSUPPORTED;
 }
-// The workspace of the calls that need switch_backward_workspace_size bytes.
+// The workspace of the calls that need the backward's regions.
 static switch_status_t check_bwd_workspace(const switch_config_t* cfg, int64_t C, const void* ws,
                                            size_t ws_bytes) {
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
@@ -1140,7 +1160,7 @@ switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
   a.err = c.err;
   a.spin = c.spin;
   a.num_sms = c.num_sms;
-  const SplitPlan split = split_plan(*cfg, c.C);
+  const SplitPlan split = split_plan(*cfg, c.C, ws_bytes - c.L.ybuf, 0);
   a.parts1 = split.q8_hidden;
   a.parts2 = split.q8_out;
   a.part = c.at<float>(c.L.ybuf);
@@ -1191,7 +1211,7 @@ switch_status_t switch_expert_ffn_checkpoint(const switch_config_t* cfg, const v
                                 cfg->T, dispatched ? nullptr : c.ws + c.L.xdisp, false,
                                 static_cast<uint8_t*>(xq), static_cast<uint8_t*>(x_scale), c.err,
                                 c.st));
-  const SplitPlan split = split_plan(*cfg, c.C);
+  const SplitPlan split = split_plan(*cfg, c.C, ws_bytes - c.L.ybuf, 0);
   RowsGemmArgs a = rows_args(cfg, c, counts);
   a.part = c.at<float>(c.L.ybuf);
   a.parts = split.hidden;
@@ -1229,22 +1249,24 @@ switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const 
     return SWITCH_ERR_INVALID_ARG;
   s = check_bwd_workspace(cfg, C, ws, ws_bytes);
   if (s != SWITCH_OK) return s;
+  const size_t scratch = bwd_q8_scratch(*cfg, C, layout_for(*cfg, C));
+  if (ws_bytes < scratch) return SWITCH_ERR_WORKSPACE_TOO_SMALL;
   s = prepare(cfg, ws, ws_bytes, stream, &c);
   if (s != SWITCH_OK) return s;
   const int64_t S = static_cast<int64_t>(cfg->n_experts) * c.C;
   const int d = cfg->d_model, F = cfg->d_ff;
   uint8_t* xb = c.ws + c.L.xdisp;
   uint8_t* hb = c.ws + c.L.hbuf;
-  uint32_t* mask = c.at<uint32_t>(c.L.mask);
+  uint32_t* mask = c.at<uint32_t>(mask_tail(*cfg, C) ? c.L.dgp : c.L.ybuf);
   const UnpackSet sets[2] = {{F, static_cast<const uint8_t*>(hq),
                               static_cast<const uint8_t*>(h_scale), hb, mask},
                              {d, static_cast<const uint8_t*>(xq),
                               static_cast<const uint8_t*>(x_scale), xb, nullptr}};
   SMOE_TRY(launch_unpack_rows(S, counts, c.C, false, sets, 2, c.st));
   // da = (dy w2) where h > 0, dx = da w1, dw1 = da^T x, dw2 = dy^T h
-  const SplitPlan split = split_plan(*cfg, c.C);
+  const SplitPlan split = split_plan(*cfg, c.C, 0, ws_bytes - scratch);
   RowsGemmArgs a = rows_args(cfg, c, counts);
-  a.part = c.at<float>(c.L.part);
+  a.part = c.at<float>(scratch);
   a.parts = split.da;
   a.n_out = F;
   a.K = d;
@@ -1278,7 +1300,7 @@ switch_status_t switch_expert_ffn_backward_q8(const switch_config_t* cfg, const 
   g.b[1] = hb;
   g.dw[1] = dw2;
   g.parts = split.grads;
-  g.part = c.at<float>(c.L.part);
+  g.part = c.at<float>(scratch);
   return cuda_status(launch_weight_grads(g, c.st));
 }
 
