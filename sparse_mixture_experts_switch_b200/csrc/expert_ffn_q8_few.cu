@@ -3,7 +3,7 @@
 // are streams of weights, bound by memory and its latency: no tiles in shared
 // memory and no TMEM, but weight rows loaded straight into the registers of
 // warp-level MMAs (m16n8k32, e4m3, fp32 sums): 16 features x 8 tokens a warp (an
-// expert with more rows, which only rows dispatched by other means can be, takes
+// expert whose slots the caller gave more rows, tokens named more than once, takes
 // them eight at a time).
 //
 // A lane loads 16 consecutive bytes of a row, so a quad reads 64 and the order of
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(RG * S * 32, 2) few_gemm_kernel(FewParams p) {
 }  // namespace
 
 cudaError_t launch_expert_ffn_q8_few(const FfnQ8Args& a, cudaStream_t st) {
-  // at most min(A, N) experts hold tokens; two CTAs an SM
+  // at most min(rows, N) experts hold tokens; two CTAs an SM
   const int64_t experts = a.A < a.N ? a.A : a.N;
   auto grid = [&](int tiles) {
     const int64_t items = experts * tiles, most = 2 * a.num_sms;

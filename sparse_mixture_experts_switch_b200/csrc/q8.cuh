@@ -181,7 +181,7 @@ cudaError_t launch_quantize_weights(int64_t n, int rows, int cols, const void* w
 
 // The experts' FFNs on 8-bit rows and weights (expert_ffn_q8.cu).
 struct FfnQ8Args {
-  int64_t A, T;              // assignments (tokens x routes), tokens
+  int64_t A, T;              // most kept rows, tokens
   int d, F, N;
   int64_t C;
   const uint8_t* xq;         // [N*C, d]; few: [T, d], or by slots with slot_token null
@@ -200,7 +200,7 @@ struct FfnQ8Args {
   int num_sms;
 };
 cudaError_t launch_expert_ffn_q8(const FfnQ8Args& a, cudaStream_t st);
-// The same for a batch of at most kFewTokens assignments (expert_ffn_q8_few.cu):
+// The same for few rows, by and large kFewTokens assignments (expert_ffn_q8_few.cu):
 // reads the tokens' rows through slot_token itself; hw holds row-major scale
 // bytes.  Measured against the tensor-core tiles, experts of 1024 x 4096: 8
 // assignments of 128 experts 24.3 against 33.6 us, of one expert 14.4 against

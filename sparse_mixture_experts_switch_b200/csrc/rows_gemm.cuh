@@ -58,8 +58,8 @@ inline int parts_of(int64_t stages, int64_t most, double bytes) {
   const double gain = kStageUs * static_cast<double>(stages) * (1 - 1 / sd) - sd * bytes / kBytesPerUs;
   return gain > kLaunchUs ? static_cast<int>(s) : 1;
 }
-// A product over experts' rows: n_out results of the kept rows (A assignments at
-// most), `stages` stages of 128 bf16 or 256 codes each; scratch of at most `room` bytes.
+// A product over experts' rows: n_out results of the kept rows (A at most), `stages`
+// stages of 128 bf16 or 256 codes each; scratch of at most `room` bytes.
 inline int sum_parts(int64_t N, int64_t C, int64_t A, int64_t n_out, int64_t stages, size_t room) {
   if (A <= 0 || C <= 0) return 1;
   const int64_t tiles = std::min(std::min(N, A) + A / 256, N * ((C + 255) / 256)) *
@@ -68,7 +68,8 @@ inline int sum_parts(int64_t N, int64_t C, int64_t A, int64_t n_out, int64_t sta
   return parts_of(stages, std::min(kSplitPairs / tiles, most / (4 * N * C * n_out)),
                   4.0 * static_cast<double>(std::min(A, N * C)) * static_cast<double>(n_out));
 }
-// Most parts of the weight gradients' sums over an expert's rows, and those of an
+// Most parts of the weight gradients' sums over an expert's rows (by an even share of
+// the batch's A assignments; sums of more rows take no more parts), and those of an
 // expert with `stages` stages (64 rows each).
 inline int grad_parts(int64_t N, int64_t C, int64_t A, int64_t d, int64_t F, size_t room) {
   const int64_t tiles = 2 * N * ((d + 255) / 256) * ((F + 255) / 256);

@@ -65,6 +65,23 @@ int ntiles_of(int64_t T) { return static_cast<int>((T + kTileTok - 1) / kTileTok
 // routes x T (token, expert) assignments, route-major.
 int routes_of(const switch_config_t& c) { return (c.flags & SWITCH_FLAG_TOP2) ? 2 : 1; }
 
+// Most kept rows of all experts: the batch's assignments, or, where the caller laid
+// the rows into their slots (by whatever means), the slots.
+int64_t most_rows(const switch_config_t& c, int64_t C) {
+  return (c.flags & SWITCH_FLAG_ROWS_DISPATCHED) ? c.n_experts * C : routes_of(c) * c.T;
+}
+
+// The 8-bit FFN by the kernels for few tokens: at most kFewTokens assignments.  Rows
+// that are dispatched already may be more than the config's tokens: then by an
+// expert's slots, which those kernels take at once, and by the experts, whose
+// weights they stream.  Measured with 8 slots an expert of 1024 x 4096, 8 rows in all
+// and every slot full, against the tiles: 4 experts 14.3 and 14.3 us (22.4, 22.6), 16
+// experts 20.5 and 45 (24.8, 41), 128 experts 24.6 and 297 (27.8, 199).
+bool few_tokens(const switch_config_t& c, int64_t C) {
+  if (routes_of(c) * c.T > kFewTokens) return false;
+  return !(c.flags & SWITCH_FLAG_ROWS_DISPATCHED) || (C <= kFewTokens && c.n_experts <= 16);
+}
+
 // Parts of the sums of the expert FFNs' products with 8-bit rows, and the bytes
 // of scratch they take: at most `fwd_room` and `bwd_room`.
 struct SplitPlan {
@@ -74,14 +91,14 @@ struct SplitPlan {
 SplitPlan split_plan(const switch_config_t& c, int64_t C, size_t fwd_room, size_t bwd_room) {
   SplitPlan s{1, 1, 1, 1, 1, 1, 1, 0, 0};
   if (c.dtype != SWITCH_BF16) return s;
-  const int64_t A = routes_of(c) * c.T, N = c.n_experts, d = c.d_model, F = c.d_ff;
+  const int64_t A = most_rows(c, C), N = c.n_experts, d = c.d_model, F = c.d_ff;
   s.q8_hidden = sum_parts(N, C, A, F, (d + 255) / 256, fwd_room);
   s.q8_out = sum_parts(N, C, A, d, (F + 255) / 256, fwd_room);
   s.hidden = sum_parts(N, C, A, F, (d + 127) / 128, fwd_room);
   s.out = sum_parts(N, C, A, d, (F + 127) / 128, fwd_room);
   s.da = sum_parts(N, C, A, F, (d + 127) / 128, bwd_room);
   s.dx = sum_parts(N, C, A, d, (F + 127) / 128, bwd_room);
-  s.grads = grad_parts(N, C, A, d, F, bwd_room);
+  s.grads = grad_parts(N, C, routes_of(c) * c.T, d, F, bwd_room);
   auto bytes = [&](int64_t parts, int64_t values) {
     return parts > 1 ? sizeof(float) * parts * values : size_t{0};
   };
@@ -1139,7 +1156,7 @@ switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
   if (s != SWITCH_OK) return s;
   const int64_t S = static_cast<int64_t>(cfg->n_experts) * c.C;
   FfnQ8Args a{};
-  a.A = routes_of(*cfg) * cfg->T;
+  a.A = most_rows(*cfg, c.C);
   a.d = cfg->d_model;
   a.F = cfg->d_ff;
   a.N = cfg->n_experts;
@@ -1165,7 +1182,7 @@ switch_status_t switch_expert_ffn_q8(const switch_config_t* cfg, const void* xq,
   a.parts2 = split.q8_out;
   a.part = c.at<float>(c.L.ybuf);
   a.xq = static_cast<const uint8_t*>(xq);
-  if (a.A <= kFewTokens) {
+  if (few_tokens(*cfg, c.C)) {
     a.xs = static_cast<const uint8_t*>(x_scale);
     a.slot_token = dispatched ? nullptr : slot_token;
     return cuda_status(launch_expert_ffn_q8_few(a, c.st));
