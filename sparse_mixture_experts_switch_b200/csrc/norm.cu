@@ -404,7 +404,9 @@ __global__ void __launch_bounds__(kNormThreads) residual_norm_bwd_wide_kernel(No
   }
 }
 
-// Wide rows: column sums of dy z rstd over the rows blockIdx.y, + gridDim.y, ...
+// Wide rows: column sums of dy z rstd over the rows blockIdx.y, + gridDim.y, ...; runs
+// of 64 rows are summed by themselves and then added (one running sum's error would
+// grow with the rows: 170 2^-24 over 1024 equal terms of 0.7, so 12).
 template <bool kBf16>
 __global__ void __launch_bounds__(kNormThreads) gain_columns_kernel(NormBwdArgs a) {
   using R = Row<kBf16>;
@@ -412,20 +414,29 @@ __global__ void __launch_bounds__(kNormThreads) gain_columns_kernel(NormBwdArgs 
   const int nv = a.d / kPer;
   const int v = blockIdx.x * kNormThreads + threadIdx.x;
   if (v >= nv) return;
-  float acc[kPer];
+  float acc[kPer], run[kPer];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) acc[j] = 0.f;
+  for (int j = 0; j < kPer; ++j) acc[j] = run[j] = 0.f;
+  int n = 0;
   for (int64_t r = blockIdx.y; r < a.T; r += gridDim.y) {
     float z[kPer], y[kPer];
     R::get(reinterpret_cast<const uint4*>(a.z)[r * nv + v], z);
     R::get(reinterpret_cast<const uint4*>(a.dy)[r * nv + v], y);
     const float rstd = a.rstd[r];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) acc[j] = fmaf(y[j] * z[j], rstd, acc[j]);
+    for (int j = 0; j < kPer; ++j) run[j] = fmaf(y[j] * z[j], rstd, run[j]);
+    if (++n == 64) {
+      n = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        acc[j] += run[j];
+        run[j] = 0.f;
+      }
+    }
   }
 #pragma unroll
   for (int j = 0; j < kPer; ++j)
-    a.part[static_cast<int64_t>(blockIdx.y) * a.d + v * kPer + j] = acc[j];
+    a.part[static_cast<int64_t>(blockIdx.y) * a.d + v * kPer + j] = acc[j] + run[j];
 }
 
 // dgain[c] = sum of the nparts rows of `part`: a block takes 32 columns, each of
