@@ -19,7 +19,13 @@
 // outputs and the sum, V = 2 and eight blocks an SM in turn 52.4 us, V = 4 and two
 // blocks 53.4, three blocks of 80 registers (spilling) 61 (302 MB: 46.3 at the
 // copy rate); backward with its second gradient, V = 4 and two resident blocks an
-// SM 55.5 us, four blocks queued 61.8, V = 2 62.2 (268 MB: 41.1).
+// SM 55.5 us, four blocks queued 61.8, V = 2 62.2 (268 MB: 41.1).  Short launches wait
+// on latency: 5003 x 772 fp32 forward (31 MB: 4.7 us) 10.3 us, as 193 vectors fill 256
+// lane slots and each of 1184 blocks, 592 resident, takes two or three pairs of rows
+// with a barrier in each; 517 x 4096 fp32 backward (25 MB: 3.9) 12.5 us, as a block loads
+// its second row after the first one's barrier, and dgain's reduction follows.  Wide rows,
+// bf16: 4096 x 8256 forward 76.8 us (304 MB: 46.6), backward 93.8 (203 MB: 31.1; z and dy
+// are read three times), 4096 x 20480 170 and 176 (116, 77).
 #include "q8.cuh"
 
 namespace smoe {

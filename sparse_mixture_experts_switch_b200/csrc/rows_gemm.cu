@@ -8,6 +8,13 @@
 //   kRowsStore   y = h W2_e^T, or dx = da W1_e;
 //   kRowsMask    da = (dy W2_e) where h > 0 (a bit per value).
 //
+// Sums are fp32 in TMEM; each result is rounded once, to bf16.  So is da, the operand
+// of the two products behind it: kept in two bf16 terms it would double the bytes
+// and the MMAs of both.  It costs a factor of the square root of two in the error of
+// dx and dw1 (2.3e-3 of the norm against 1.7e-3, the rounding of the result alone),
+// as in the layer's own backward pass.  Hidden values near a border between two bf16
+// numbers may fall to either side with the order of the fp32 sum.
+//
 // The walk, the roles and the reasons are those of the 8-bit products
 // (expert_ffn_q8.cu): CTA pairs, the weights as the MMA's M (256 features a
 // tile), up to 256 of an expert's tokens as its N, warp-uniform issue loops, two

@@ -14,7 +14,10 @@
 // one expert of 64 x 9472, 31.1 and 39.2 us; backward of 146 tokens, two experts of 960
 // x 7744, 64 and 82; of 30000 tokens, one expert of 256 x 256, 78 and 179; but of 512
 // tokens, one expert of 1024 x 4096 (10 MB of sums for 32 stages), 47.6 and 45.0, and
-// of 3000, two experts of 256 x 1024, 38.4 and 33.6: those stay whole.
+// of 3000, two experts of 256 x 1024, 38.4 and 33.6: those stay whole.  Of 260 drawn
+// sizes (1 to 32768 tokens, widths from 64) 27 have a sum in parts: against the same
+// sums whole 20 of them gain 5 to 37%, none loses.  Where the workspace has no room
+// for all parts, there are as many as it holds, or the sum stays whole.
 #include "rows_gemm.cuh"
 
 namespace smoe {

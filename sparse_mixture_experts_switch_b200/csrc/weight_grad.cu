@@ -19,7 +19,8 @@
 // Measured alone, 128 experts of 1024 x 4096, 25278 kept rows, both gradients (2.15
 // GB written, 0.5 read): 534 us, 565 without the fetch of later tiles into L2; the
 // same stores without any rows take 411 us (5.2 TB/s).  Stores by the drain warps'
-// own instructions instead of TMA boxes took 550.
+// own instructions instead of TMA boxes took 550.  Launches of the same build on the
+// same buffers' sizes range from 534 to 625 us (26163 rows), so compare medians.
 #include <cstring>
 
 #include "rows_gemm.cuh"
